@@ -2,7 +2,8 @@
 
 Causal / sliding-window / full grouped-query prefill (contiguous, or the
 newest positions against a paged context) and paged single-token decode (whole
-cache, or a sliding window with sink positions and learned sink logits),
+cache, or a sliding window with sink positions and learned sink logits), with
+the block tables, slot maps and query/key norms and rotations around them,
 computed by hand-written CUDA kernels behind the C ABI of
 ``include/attn.h``. This module is the thin Python binding: it checks tensor
 dtypes, shapes and devices, allocates outputs with PyTorch (device memory
@@ -14,6 +15,7 @@ is no CPU or PyTorch fallback, and calls raise if the library is not built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -25,7 +27,8 @@ MASKS = {"full": 0, "causal": 1, "window": 2, "sliding_window": 2}
 
 __all__ = ["prefill", "prefill_paged", "decode_paged", "decode_paged_window", "paged_gather", "decode_plan",
            "decode_workspace_bytes", "decode_window_workspace_bytes", "mla_decode_paged", "mla_decode_workspace_bytes",
-           "prefill_backward", "prefill_backward_workspace_bytes",
+           "prefill_backward", "prefill_backward_workspace_bytes", "paged_extend", "paged_release", "qk_norm_rope",
+           "qk_norm_rope_paged", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_bytes",
            "AttnError", "version"]
 
 
@@ -364,3 +367,297 @@ def paged_gather(cache, block_table, seq_lens, max_seq_len: int, out=None, statu
                                       _stream_handle(stream))
     _lib.check(rc, "attn_paged_gather")
     return out
+
+
+def _entry(fn):
+    """Runs fn with the device of its first argument current and, when the
+    caller names a stream, with that stream current: outputs and workspaces
+    then come from that stream's memory, so nothing else can still be using
+    them when the kernels run."""
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError("the inputs must be CUDA tensors")
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError(f"stream is on {stream.device}, the inputs on {first.device}")
+            with torch.cuda.stream(stream):
+                return fn(first, *args, **kw)
+        if first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return fn(first, *args, **kw)
+        return fn(first, *args, **kw)
+
+    return call
+
+
+def _need_on(t, name: str, dtype, shape, dev, strided: bool = False) -> None:
+    """One input or output: dtype, exact shape, device, and contiguous unless strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not strided and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _need_dims(t, name: str, ndim: int, layout: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must be {layout}")
+
+
+def _need_status(t, dev) -> None:
+    if t is not None:
+        _need_buf(t, "status")
+        if t.device != dev:
+            raise ValueError(f"status must be on {dev}")
+
+
+def _need_workspace(t, dev) -> None:
+    if t is not None:
+        _need_buf(t, "workspace")
+        if t.device != dev:
+            raise ValueError(f"workspace must be on {dev}")
+
+
+def _out_on(t, name: str, dtype, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need_on(t, name, dtype, shape, dev)
+    return t
+
+
+def _current() -> int:
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _addr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _table_args(seq_lens, second, second_name, block_table, free_blocks, num_free, seq_lens_out, num_free_out, status):
+    _need_dims(seq_lens, "seq_lens", 1, "[B]")
+    _need_dims(block_table, "block_table", 2, "[B, max_blocks]")
+    _need_dims(free_blocks, "free_blocks", 1, "[capacity]")
+    dev, B, i32 = seq_lens.device, seq_lens.shape[0], torch.int32
+    _need_on(seq_lens, "seq_lens", i32, (B,), dev)
+    _need_on(second, second_name, i32, (B,), dev)
+    _need_on(block_table, "block_table", i32, (B, block_table.shape[1]), dev)
+    _need_on(free_blocks, "free_blocks", i32, (free_blocks.shape[0],), dev)
+    _need_on(num_free, "num_free", i32, (1,), dev)
+    _need_status(status, dev)
+    return _out_on(seq_lens_out, "seq_lens_out", i32, (B,), dev), _out_on(num_free_out, "num_free_out", i32, (1,), dev)
+
+
+@_entry
+def paged_extend(seq_lens, new_lens, block_table, free_blocks, num_free, block_size: int, num_blocks: int,
+                 max_tokens: int, seq_lens_out=None, num_free_out=None, cu_q=None, positions=None, slots=None,
+                 status=None):
+    """The block table, positions and slot map of one serving step, from the
+    requests' lengths; returns (seq_lens_out, num_free_out, cu_q, positions,
+    slots) and writes the new entries of block_table.
+
+    seq_lens, new_lens [B] int32: cached and new tokens of each sequence;
+    free_blocks int32, a stack of num_free [1] free blocks; max_tokens rows of
+    positions and slots are written, those past the new tokens as 0 and -1.
+    cu_q [B + 1]: sequence b's new tokens are rows [cu_q[b], cu_q[b + 1]).
+    seq_lens_out and num_free_out may be seq_lens and num_free themselves. A
+    sequence that cannot be served gets the length -1 - seq_lens[b] (negative)
+    and slots of -1, and sets the status bit. Keyword stream: the CUDA stream (default: the current one).
+    """
+    seq_lens_out, num_free_out = _table_args(seq_lens, new_lens, "new_lens", block_table, free_blocks, num_free,
+                                             seq_lens_out, num_free_out, status)
+    dev, B, n = seq_lens.device, seq_lens.shape[0], max(0, int(max_tokens))
+    cu_q = _out_on(cu_q, "cu_q", torch.int32, (B + 1,), dev)
+    positions = _out_on(positions, "positions", torch.int32, (n,), dev)
+    slots = _out_on(slots, "slots", torch.int32, (n,), dev)
+    rc = _lib.lib().attn_paged_extend(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                                      free_blocks.data_ptr(), num_free.data_ptr(), seq_lens_out.data_ptr(),
+                                      num_free_out.data_ptr(), cu_q.data_ptr(), positions.data_ptr(),
+                                      slots.data_ptr(), B, int(num_blocks), int(block_size), block_table.shape[1],
+                                      free_blocks.shape[0], int(max_tokens), _addr(status), _current())
+    _lib.check(rc, "attn_paged_extend")
+    return seq_lens_out, num_free_out, cu_q, positions, slots
+
+
+@_entry
+def paged_release(seq_lens, finished, block_table, free_blocks, num_free, block_size: int, num_blocks: int,
+                  seq_lens_out=None, num_free_out=None, status=None):
+    """Puts the blocks of the sequences with finished[b] != 0 (int32) back on
+    the free list; returns (seq_lens_out, num_free_out), the finished lengths 0.
+    A length -1 - L that paged_extend left counts as L. free_blocks is written from num_free on; in place as paged_extend."""
+    seq_lens_out, num_free_out = _table_args(seq_lens, finished, "finished", block_table, free_blocks, num_free,
+                                             seq_lens_out, num_free_out, status)
+    rc = _lib.lib().attn_paged_release(seq_lens.data_ptr(), finished.data_ptr(), block_table.data_ptr(),
+                                       free_blocks.data_ptr(), num_free.data_ptr(), seq_lens_out.data_ptr(),
+                                       num_free_out.data_ptr(), seq_lens.shape[0], int(num_blocks), int(block_size),
+                                       block_table.shape[1], free_blocks.shape[0], _addr(status), _current())
+    _lib.check(rc, "attn_paged_release")
+    return seq_lens_out, num_free_out
+
+
+_STRIDES6, _STRIDES9 = ctypes.c_int64 * 6, ctypes.c_int64 * 9
+
+
+def _need_heads(t, name: str, shape, dev) -> None:
+    """A [.., heads, d] view whose head rows are contiguous (a view of a fused projection is one)."""
+    _need_on(t, name, torch.bfloat16, shape, dev, strided=True)
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+
+
+def _need_heads_out(t, name: str, shape, dev) -> None:
+    _need_heads(t, name, shape, dev)
+    if any(s == 0 and n > 1 for s, n in zip(t.stride(), shape)):
+        raise ValueError(f"{name}: an output's rows may not share memory")
+
+
+def _angles(q_weight, k_weight, cos, sin, positions, pos_shape, d, dev):
+    """Checks weights, angle tables and positions; returns (weights are bf16, rotary_dim, max_pos)."""
+    w_bf16 = 0
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight come together")
+    if q_weight is not None:
+        _need_dims(q_weight, "q_weight", 1, "[d]")
+        if q_weight.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"q_weight must be float32 or bfloat16, got {q_weight.dtype}")
+        _need_on(q_weight, "q_weight", q_weight.dtype, (d,), dev)
+        _need_on(k_weight, "k_weight", q_weight.dtype, (d,), dev)
+        w_bf16 = int(q_weight.dtype == torch.bfloat16)
+    _need_dims(cos, "cos", 2, "[max_pos, rotary_dim / 2]")
+    _need_on(cos, "cos", torch.float32, cos.shape, dev)
+    _need_on(sin, "sin", torch.float32, cos.shape, dev)
+    if positions is not None:
+        _need_on(positions, "positions", torch.int32, pos_shape, dev)
+    return w_bf16, 2 * cos.shape[1], cos.shape[0]
+
+
+@_entry
+def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out=None, k_out=None, v_out=None, status=None):
+    """RMS norm of each query and key head and the position rotation in one
+    pass, into the layout of prefill(); returns (q, k, v) as [B, H, N, d].
+
+    q [B, N, Hq, d], k and v [B, N, Hkv, d] bf16 (views of a fused projection
+    are fine: only a head's elements must be contiguous); q_weight, k_weight
+    [d] fp32 or bf16, both None for no norm; cos, sin [max_pos, rotary_dim / 2]
+    fp32; positions [B, N] int32 (default 0 .. N - 1). The first rotary_dim
+    elements turn in pairs (f, f + rotary_dim / 2), or (2 f, 2 f + 1) when
+    interleaved. Keyword stream as in paged_extend.
+    """
+    _need_dims(q, "q", 4, "[B, N, Hq, d]")
+    _need_dims(k, "k", 4, "[B, N, Hkv, d]")
+    dev, (B, N, Hq, d), Hkv = q.device, q.shape, k.shape[2]
+    _need_heads(q, "q", (B, N, Hq, d), dev)
+    _need_heads(k, "k", (B, N, Hkv, d), dev)
+    _need_heads(v, "v", (B, N, Hkv, d), dev)
+    w_bf16, rd, max_pos = _angles(q_weight, k_weight, cos, sin, positions, (B, N), d, dev)
+    _need_status(status, dev)
+    q_out = _out_on(q_out, "q_out", torch.bfloat16, (B, Hq, N, d), dev)
+    k_out = _out_on(k_out, "k_out", torch.bfloat16, (B, Hkv, N, d), dev)
+    v_out = _out_on(v_out, "v_out", torch.bfloat16, (B, Hkv, N, d), dev)
+    rc = _lib.lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                      _STRIDES9(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
+                                      _addr(q_weight), _addr(k_weight), w_bf16, cos.data_ptr(), sin.data_ptr(),
+                                      _addr(positions), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, N,
+                                      Hq, Hkv, d, rd, max_pos, float(eps), int(interleaved), _addr(status),
+                                      _current())
+    _lib.check(rc, "attn_qk_norm_rope")
+    return q_out, k_out, v_out
+
+
+@_entry
+def qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, eps: float = 1e-6,
+                       interleaved: bool = False, q_out=None, status=None):
+    """The serving form of qk_norm_rope: packed tokens q [T, Hq, d], k and v
+    [T, Hkv, d]; returns q [T, Hq, d] and writes the keys and values into the
+    caches [num_blocks, block_size, Hkv, d] at slots [T] (int32, -1: nowhere;
+    no slot twice). positions and slots are paged_extend's."""
+    _need_dims(q, "q", 3, "[T, Hq, d]")
+    _need_dims(k, "k", 3, "[T, Hkv, d]")
+    dev, (T, Hq, d), Hkv = q.device, q.shape, k.shape[1]
+    _need_heads(q, "q", (T, Hq, d), dev)
+    _need_heads(k, "k", (T, Hkv, d), dev)
+    _need_heads(v, "v", (T, Hkv, d), dev)
+    if positions is None or slots is None:
+        raise TypeError("positions and slots must be int32 tensors")
+    w_bf16, rd, max_pos = _angles(q_weight, k_weight, cos, sin, positions, (T,), d, dev)
+    _need_on(slots, "slots", torch.int32, (T,), dev)
+    _need_dims(k_cache, "k_cache", 4, "[num_blocks, block_size, Hkv, d]")
+    num_blocks, block_size = k_cache.shape[:2]
+    _need_on(k_cache, "k_cache", torch.bfloat16, (num_blocks, block_size, Hkv, d), dev)
+    _need_on(v_cache, "v_cache", torch.bfloat16, (num_blocks, block_size, Hkv, d), dev)
+    _need_status(status, dev)
+    q_out = _out_on(q_out, "q_out", torch.bfloat16, (T, Hq, d), dev)
+    if T == 0:
+        return q_out
+    rc = _lib.lib().attn_qk_norm_rope_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                            _STRIDES6(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2]),
+                                            _addr(q_weight), _addr(k_weight), w_bf16, cos.data_ptr(), sin.data_ptr(),
+                                            positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(),
+                                            k_cache.data_ptr(), v_cache.data_ptr(), T, Hq, Hkv, d, num_blocks,
+                                            block_size, rd, max_pos, float(eps), int(interleaved), _addr(status),
+                                            _current())
+    _lib.check(rc, "attn_qk_norm_rope_paged")
+    return q_out
+
+
+def qk_norm_rope_backward_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, d: int) -> int:
+    n = int(_lib.lib().attn_qk_norm_rope_backward_workspace_bytes(B, N, Hq, Hkv, d))
+    if n == 0:
+        raise AttnError(_lib.ATTN_ERR_INVALID_ARG, "attn_qk_norm_rope_backward_workspace_bytes")
+    return n
+
+
+@_entry
+def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, positions=None, eps: float = 1e-6,
+                          interleaved: bool = False, dq=None, dk=None, dv=None, workspace=None, status=None):
+    """Gradients of qk_norm_rope() from those of its outputs, d_q [B, Hq, N, d],
+    d_k and d_v [B, Hkv, N, d] (what prefill_backward returns): (dq, dk, dv,
+    dq_weight, dk_weight), the weights' in fp32, or None without weights.
+
+    dq [B, N, Hq, d], dk and dv [B, N, Hkv, d] come as views of one fused
+    [B, N, Hq + 2 Hkv, d] gradient unless given (any strides with contiguous
+    head rows). q, k: the forward's inputs.
+    """
+    _need_dims(q, "q", 4, "[B, N, Hq, d]")
+    _need_dims(k, "k", 4, "[B, N, Hkv, d]")
+    dev, (B, N, Hq, d), Hkv, bf16 = q.device, q.shape, k.shape[2], torch.bfloat16
+    _need_heads(q, "q", (B, N, Hq, d), dev)
+    _need_heads(k, "k", (B, N, Hkv, d), dev)
+    _need_on(d_q, "d_q", bf16, (B, Hq, N, d), dev)
+    _need_on(d_k, "d_k", bf16, (B, Hkv, N, d), dev)
+    _need_on(d_v, "d_v", bf16, (B, Hkv, N, d), dev)
+    w_bf16, rd, max_pos = _angles(q_weight, k_weight, cos, sin, positions, (B, N), d, dev)
+    _need_status(status, dev)
+    if dq is None and dk is None and dv is None:
+        fused = torch.empty((B, N, Hq + 2 * Hkv, d), dtype=bf16, device=dev)
+        dq, dk, dv = fused[:, :, :Hq], fused[:, :, Hq:Hq + Hkv], fused[:, :, Hq + Hkv:]
+    dq = torch.empty((B, N, Hq, d), dtype=bf16, device=dev) if dq is None else dq
+    dk = torch.empty((B, N, Hkv, d), dtype=bf16, device=dev) if dk is None else dk
+    dv = torch.empty((B, N, Hkv, d), dtype=bf16, device=dev) if dv is None else dv
+    _need_heads_out(dq, "dq", (B, N, Hq, d), dev)
+    _need_heads_out(dk, "dk", (B, N, Hkv, d), dev)
+    _need_heads_out(dv, "dv", (B, N, Hkv, d), dev)
+    dwq = dwk = None
+    if q_weight is not None:
+        dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=dev).unbind()
+        if workspace is None:
+            workspace = torch.empty(qk_norm_rope_backward_workspace_bytes(B, N, Hq, Hkv, d), dtype=torch.uint8,
+                                    device=dev)
+    _need_workspace(workspace, dev)
+    rc = _lib.lib().attn_qk_norm_rope_backward(
+        q.data_ptr(), k.data_ptr(), _STRIDES6(*q.stride()[:3], *k.stride()[:3]), _addr(q_weight), _addr(k_weight),
+        w_bf16, cos.data_ptr(), sin.data_ptr(), _addr(positions), d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _STRIDES9(*dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]),
+        _addr(dwq), _addr(dwk), B, N, Hq, Hkv, d, rd, max_pos, float(eps), int(interleaved), _addr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _addr(status), _current())
+    _lib.check(rc, "attn_qk_norm_rope_backward")
+    return dq, dk, dv, dwq, dwk

@@ -26,6 +26,12 @@ SYMBOLS = (
     "attn_prefill_backward",
     "attn_mla_decode_workspace_bytes",
     "attn_mla_decode_paged",
+    "attn_paged_extend",
+    "attn_paged_release",
+    "attn_qk_norm_rope",
+    "attn_qk_norm_rope_paged",
+    "attn_qk_norm_rope_backward_workspace_bytes",
+    "attn_qk_norm_rope_backward",
     "attn_paged_gather",
     "attn_status_string",
     "attn_version",
@@ -49,6 +55,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_strides = ctypes.POINTER(ctypes.c_int64)  # host array of element strides
 
 
 def _declare(lib):
@@ -84,6 +91,21 @@ def _declare(lib):
     lib.attn_mla_decode_paged.restype = _i
     lib.attn_paged_gather.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp]
     lib.attn_paged_gather.restype = _i
+    lib.attn_paged_extend.argtypes = [_vp] * 10 + [_i] * 6 + [_vp, _vp]
+    lib.attn_paged_extend.restype = _i
+    lib.attn_paged_release.argtypes = [_vp] * 7 + [_i] * 5 + [_vp, _vp]
+    lib.attn_paged_release.restype = _i
+    lib.attn_qk_norm_rope.argtypes = [_vp, _vp, _vp, _strides, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp] + \
+        [_i] * 7 + [_f, _i, _vp, _vp]
+    lib.attn_qk_norm_rope.restype = _i
+    lib.attn_qk_norm_rope_paged.argtypes = [_vp, _vp, _vp, _strides, _vp, _vp, _i] + [_vp] * 7 + [_i] * 8 + \
+        [_f, _i, _vp, _vp]
+    lib.attn_qk_norm_rope_paged.restype = _i
+    lib.attn_qk_norm_rope_backward_workspace_bytes.argtypes = [_i] * 5
+    lib.attn_qk_norm_rope_backward_workspace_bytes.restype = _sz
+    lib.attn_qk_norm_rope_backward.argtypes = [_vp, _vp, _strides, _vp, _vp, _i] + [_vp] * 9 + \
+        [_strides, _vp, _vp] + [_i] * 7 + [_f, _i, _vp, _sz, _vp, _vp]
+    lib.attn_qk_norm_rope_backward.restype = _i
     lib.attn_status_string.argtypes = [_i]
     lib.attn_status_string.restype = ctypes.c_char_p
     lib.attn_version.argtypes = []

@@ -34,6 +34,7 @@ long long wait_budget_cycles() {
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int current_sm_count(int* out) {
   int dev = 0;
@@ -179,6 +180,50 @@ int decode_common(const void* q, const void* k_cache, const void* v_cache, const
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// Table sizes: positions, slots and sums of blocks are 32-bit, and a CTA keeps
+// three values per sequence in shared memory.
+bool table_sizes_fit(int B, int num_blocks, int block_size, int max_blocks_per_seq) {
+  const long long most = (1LL << 31) - 1;
+  return B <= kMaxTableSeqs && static_cast<long long>(num_blocks) * block_size <= most &&
+         static_cast<long long>(max_blocks_per_seq) * block_size <= most &&
+         static_cast<long long>(B) * max_blocks_per_seq <= most;
+}
+
+// Checks shared by the norm and rotation entry points. strides: (sequence,
+// token, head) of q, k, v in elements; a head row is contiguous.
+int norm_rope_args(const void* q, const void* k, const void* v, const int64_t* strides, const void* q_weight,
+                   const void* k_weight, int weight_bf16, const float* cos_table, const float* sin_table,
+                   const int32_t* positions, int B, int N, int Hq, int Hkv, int d, int rotary_dim, int max_pos,
+                   float eps, int interleaved, NormRopeArgs* a) {
+  if (!strides || !cos_table || !sin_table) return ATTN_ERR_INVALID_ARG;
+  if ((q_weight == nullptr) != (k_weight == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || max_pos <= 0) return ATTN_ERR_INVALID_ARG;
+  if (!positions && max_pos < N) return ATTN_ERR_INVALID_ARG;
+  if (q_weight && (!(eps >= 0.f) || !std::isfinite(eps))) return ATTN_ERR_INVALID_ARG;
+  for (const void* p : {q, k, v, q_weight, k_weight, (const void*)cos_table, (const void*)sin_table})
+    if (!aligned16(p)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(positions)) return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 9; ++i)
+    if (strides[i] % 8 != 0) return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (rotary_dim <= 0 || rotary_dim > d) return ATTN_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hkv > 65535 ||
+      static_cast<long long>(B) * N > ((1LL << 31) - 1) / norm_rope_chunks(Hq, Hkv))
+    return ATTN_ERR_UNSUPPORTED;
+  const void* x[3] = {q, k, v};
+  for (int t = 0; t < 3; ++t) {
+    a->x[t] = x[t];
+    a->sb[t] = strides[3 * t], a->sn[t] = strides[3 * t + 1], a->sh[t] = strides[3 * t + 2];
+  }
+  a->w[0] = q_weight, a->w[1] = k_weight, a->w_bf16 = weight_bf16 != 0;
+  a->cos_t = cos_table, a->sin_t = sin_table, a->positions = positions;
+  a->B = B, a->N = N, a->Hq = Hq, a->Hkv = Hkv, a->d = d, a->rd = rotary_dim, a->max_pos = max_pos;
+  a->interleaved = interleaved != 0;
+  a->eps = eps;
+  return ATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -276,6 +321,120 @@ int attn_mla_decode_paged(const void* q, const void* cache, const int32_t* block
   return launch_mla_decode(q, cache, block_table, seq_lens, o, lse, B, H, num_blocks, block_size,
                            max_blocks_per_seq, max_seq_len, scale, workspace, plan, status,
                            reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_paged_extend(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
+                      const int32_t* free_blocks, const int32_t* num_free, int32_t* seq_lens_out,
+                      int32_t* num_free_out, int32_t* cu_q, int32_t* positions, int32_t* slots, int B, int num_blocks,
+                      int block_size, int max_blocks_per_seq, int free_capacity, int max_tokens, int32_t* status,
+                      attn_stream_t stream) {
+  if (!seq_lens || !new_lens || !block_table || !free_blocks || !num_free || !seq_lens_out || !num_free_out || !cu_q)
+    return ATTN_ERR_INVALID_ARG;
+  if (max_tokens < 0 || (max_tokens > 0 && (!positions || !slots))) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 || free_capacity <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)seq_lens, (const void*)new_lens, (const void*)block_table,
+                        (const void*)free_blocks, (const void*)num_free, (const void*)seq_lens_out,
+                        (const void*)num_free_out, (const void*)cu_q, (const void*)positions, (const void*)slots})
+    if (!aligned4(p)) return ATTN_ERR_INVALID_ARG;
+  if (!table_sizes_fit(B, num_blocks, block_size, max_blocks_per_seq)) return ATTN_ERR_UNSUPPORTED;
+  return launch_paged_extend(seq_lens, new_lens, block_table, free_blocks, num_free, seq_lens_out, num_free_out, cu_q,
+                             positions, slots, B, num_blocks, block_size, max_blocks_per_seq, free_capacity,
+                             max_tokens, status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_paged_release(const int32_t* seq_lens, const int32_t* finished, const int32_t* block_table,
+                       int32_t* free_blocks, const int32_t* num_free, int32_t* seq_lens_out, int32_t* num_free_out,
+                       int B, int num_blocks, int block_size, int max_blocks_per_seq, int free_capacity,
+                       int32_t* status, attn_stream_t stream) {
+  if (!seq_lens || !finished || !block_table || !free_blocks || !num_free || !seq_lens_out || !num_free_out)
+    return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || num_blocks <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 || free_capacity <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)seq_lens, (const void*)finished, (const void*)block_table,
+                        (const void*)free_blocks, (const void*)num_free, (const void*)seq_lens_out,
+                        (const void*)num_free_out})
+    if (!aligned4(p)) return ATTN_ERR_INVALID_ARG;
+  if (!table_sizes_fit(B, num_blocks, block_size, max_blocks_per_seq)) return ATTN_ERR_UNSUPPORTED;
+  return launch_paged_release(seq_lens, finished, block_table, free_blocks, num_free, seq_lens_out, num_free_out, B,
+                              num_blocks, block_size, max_blocks_per_seq, free_capacity, status,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_qk_norm_rope(const void* q, const void* k, const void* v, const int64_t* strides, const void* q_weight,
+                      const void* k_weight, int weight_bf16, const float* cos_table, const float* sin_table,
+                      const int32_t* positions, void* q_out, void* k_out, void* v_out, int B, int N, int Hq, int Hkv,
+                      int d, int rotary_dim, int max_pos, float eps, int interleaved, int32_t* status,
+                      attn_stream_t stream) {
+  NormRopeArgs a;
+  const int rc = norm_rope_args(q, k, v, strides, q_weight, k_weight, weight_bf16, cos_table, sin_table, positions, B,
+                                N, Hq, Hkv, d, rotary_dim, max_pos, eps, interleaved, &a);
+  if (rc != ATTN_OK) return rc;
+  if (!q_out || !k_out || !v_out || !aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out))
+    return ATTN_ERR_INVALID_ARG;
+  if (!q || !k || !v) return ATTN_ERR_INVALID_ARG;
+  return launch_norm_rope(a, q_out, k_out, v_out, nullptr, 0, status, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, const int64_t* strides, const void* q_weight,
+                            const void* k_weight, int weight_bf16, const float* cos_table, const float* sin_table,
+                            const int32_t* positions, const int32_t* slots, void* q_out, void* k_cache, void* v_cache,
+                            int T, int Hq, int Hkv, int d, int num_blocks, int block_size, int rotary_dim,
+                            int max_pos, float eps, int interleaved, int32_t* status, attn_stream_t stream) {
+  if (!strides) return ATTN_ERR_INVALID_ARG;
+  const int64_t dense[9] = {0, strides[0], strides[1], 0, strides[2], strides[3], 0, strides[4], strides[5]};
+  NormRopeArgs a;
+  const int rc = norm_rope_args(q, k, v, dense, q_weight, k_weight, weight_bf16, cos_table, sin_table, positions, 1,
+                                T, Hq, Hkv, d, rotary_dim, max_pos, eps, interleaved, &a);
+  if (rc != ATTN_OK) return rc;
+  if (!q || !k || !v || !positions || !slots || !q_out || !k_cache || !v_cache || num_blocks <= 0 || block_size <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(slots)) return ATTN_ERR_INVALID_ARG;
+  return launch_norm_rope(a, q_out, k_cache, v_cache, slots, static_cast<long long>(num_blocks) * block_size, status,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t attn_qk_norm_rope_backward_workspace_bytes(int B, int N, int Hq, int Hkv, int d) {
+  if (B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || (d != 64 && d != 128)) return 0;
+  int sms = 0;
+  if (current_sm_count(&sms) != ATTN_OK) return 0;
+  return static_cast<size_t>(norm_rope_bwd_ctas(static_cast<long long>(B) * N, Hq, Hkv, d, sms)) * 2 * d *
+         sizeof(float);
+}
+
+int attn_qk_norm_rope_backward(const void* q, const void* k, const int64_t* strides, const void* q_weight,
+                               const void* k_weight, int weight_bf16, const float* cos_table, const float* sin_table,
+                               const int32_t* positions, const void* d_q, const void* d_k, const void* d_v, void* dq,
+                               void* dk, void* dv, const int64_t* grad_strides, float* dq_weight, float* dk_weight,
+                               int B, int N, int Hq, int Hkv, int d, int rotary_dim, int max_pos, float eps,
+                               int interleaved, void* workspace, size_t workspace_bytes, int32_t* status,
+                               attn_stream_t stream) {
+  if (!strides || !grad_strides) return ATTN_ERR_INVALID_ARG;
+  const int64_t three[9] = {strides[0], strides[1], strides[2], strides[3], strides[4], strides[5], 0, 0, 0};
+  NormRopeArgs a;
+  const int rc = norm_rope_args(q, k, nullptr, three, q_weight, k_weight, weight_bf16, cos_table, sin_table,
+                                positions, B, N, Hq, Hkv, d, rotary_dim, max_pos, eps, interleaved, &a);
+  if (rc != ATTN_OK) return rc;
+  const bool norm = q_weight != nullptr;
+  if (!d_q || !d_k || !d_v || !dq || !dk || !dv) return ATTN_ERR_INVALID_ARG;
+  if (norm && (!q || !k || !dq_weight || !dk_weight)) return ATTN_ERR_INVALID_ARG;
+  for (const void* p : {d_q, d_k, d_v, (const void*)dq, (const void*)dk, (const void*)dv})
+    if (!aligned16(p)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(dq_weight) || !aligned4(dk_weight)) return ATTN_ERR_INVALID_ARG;
+  int64_t sb[3], sn[3], sh[3];
+  for (int t = 0; t < 3; ++t) {
+    sb[t] = grad_strides[3 * t], sn[t] = grad_strides[3 * t + 1], sh[t] = grad_strides[3 * t + 2];
+    if (sb[t] % 8 != 0 || sn[t] % 8 != 0 || sh[t] % 8 != 0) return ATTN_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  if (current_sm_count(&sms) != ATTN_OK) return ATTN_ERR_CUDA;
+  const int ctas = norm_rope_bwd_ctas(static_cast<long long>(B) * N, Hq, Hkv, d, sms);
+  if (norm && (!workspace || !aligned16(workspace) || workspace_bytes < static_cast<size_t>(ctas) * 2 * d * sizeof(float)))
+    return ATTN_ERR_WORKSPACE;
+  const void* const dz[3] = {d_q, d_k, d_v};
+  void* const dx[3] = {dq, dk, dv};
+  return launch_norm_rope_backward(a, dz, dx, sb, sn, sh, dq_weight, dk_weight, static_cast<float*>(workspace), ctas,
+                                   status, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int attn_paged_gather(const void* cache, const int32_t* block_table, const int32_t* seq_lens, void* out, int B,

@@ -102,4 +102,37 @@ int launch_prefill_paged(const void* q, const void* k_cache, const void* v_cache
                          int num_blocks, int block_size, int max_blocks_per_seq, int max_seq_len, int mask_kind,
                          int window, float scale, int32_t* status, cudaStream_t stream);
 
+// Block tables and slot maps from the requests' lengths (paged_tables_sm100.cu).
+constexpr int kMaxTableSeqs = 8192;  // three 32-bit values per sequence in shared memory
+int launch_paged_extend(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
+                        const int32_t* free_blocks, const int32_t* num_free, int32_t* seq_lens_out,
+                        int32_t* num_free_out, int32_t* cu_q, int32_t* positions, int32_t* slots, int B,
+                        int num_blocks, int block_size, int max_blocks_per_seq, int free_capacity, int max_tokens,
+                        int32_t* status, cudaStream_t stream);
+int launch_paged_release(const int32_t* seq_lens, const int32_t* finished, const int32_t* block_table,
+                         int32_t* free_blocks, const int32_t* num_free, int32_t* seq_lens_out, int32_t* num_free_out,
+                         int B, int num_blocks, int block_size, int max_blocks_per_seq, int free_capacity,
+                         int32_t* status, cudaStream_t stream);
+
+// Head norms and position rotation (norm_rope_sm100.cu). x: q, k, v with their
+// strides in elements (sequence, token, head); w: both null for no norm.
+struct NormRopeArgs {
+  const void* x[3];
+  int64_t sb[3], sn[3], sh[3];
+  const void* w[2];
+  int w_bf16;
+  const float *cos_t, *sin_t;
+  const int32_t* positions;
+  int B, N, Hq, Hkv, d, rd, max_pos, interleaved;
+  float eps;
+};
+int norm_rope_chunks(int Hq, int Hkv);  // groups of head rows per token
+int norm_rope_bwd_ctas(long long tokens, int Hq, int Hkv, int d, int sms);
+// slots null: outputs [B, H, N, d]; else q [T, Hq, d], k and v into the pools.
+int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_out, const int32_t* slots,
+                     long long num_slots, int32_t* status, cudaStream_t stream);
+int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], void* const dx[3], const int64_t dsb[3],
+                              const int64_t dsn[3], const int64_t dsh[3], float* dwq, float* dwk, float* dw_part,
+                              int ctas, int32_t* status, cudaStream_t stream);
+
 }  // namespace attn

@@ -1,7 +1,7 @@
 /*
  * attn.h - C ABI of the B200 (sm_100a) exact softmax attention library.
  *
- * Two operations, both exact scaled-dot-product attention
+ * Exact scaled-dot-product attention
  *     O = softmax(Q K^T * scale + M) V
  * computed with an online softmax so that the score matrix never leaves the
  * chip ("Module 5. Modern Attention Mechanisms", section 4, the SDPA
@@ -27,6 +27,11 @@
  *   attn_mla_decode_paged - absorbed Multi-head Latent Attention decode over a
  *                        paged latent cache ("Modern Attention Mechanisms",
  *                        section 7; "Module 09", the MLA section).
+ *   attn_paged_extend, attn_paged_release - block tables, positions and slot
+ *                        maps built on the GPU from the requests' lengths.
+ *   attn_qk_norm_rope (and _backward, _paged) - query and key norms with the
+ *                        position rotation, into the prefill's layout or, for
+ *                        serving, with K and V written into the paged cache.
  *
  * Conventions shared by every entry point:
  *   - Pointers named q, k, v, o, lse, k_cache, v_cache, block_table, seq_lens,
@@ -379,6 +384,177 @@ ATTN_API int attn_mla_decode_paged(const void* q, const void* cache, const int32
                                    int d_rope, int num_blocks, int block_size, int max_blocks_per_seq,
                                    int max_seq_len, float scale, void* workspace, size_t workspace_bytes,
                                    int32_t* status, attn_stream_t stream);
+
+/*
+ * attn_paged_extend - give every sequence the cache blocks its new tokens
+ * need, and say where each new token goes: one serving step's block table,
+ * positions and slot map, built on the GPU from the requests' lengths
+ * ("Module 09: Efficient Attention", "The Block Table" and the free list of
+ * "Code: A Paged KV Cache from Scratch").
+ *
+ * Sequence b grows from seq_lens[b] to seq_lens[b] + new_lens[b] tokens. Its
+ * new blocks, ceil((L + n) / block_size) - ceil(L / block_size) of them, come
+ * off the top of the free list in sequence order: the i-th block handed out is
+ * free_blocks[num_free - 1 - i]. Rows of new tokens are packed sequence after
+ * sequence: those of sequence b are [cu_q[b], cu_q[b + 1]).
+ *
+ *   seq_lens      [B] int32, cached tokens                   read
+ *   new_lens      [B] int32, new tokens (0 allowed)          read
+ *   block_table   [B, max_blocks_per_seq] int32              new entries written, the
+ *                 entry of a sequence's last, partly filled block read
+ *   free_blocks   [free_capacity] int32, a stack             read
+ *   num_free      [1] int32, blocks on it                    read
+ *   seq_lens_out  [B] int32                                  written: L + n
+ *   num_free_out  [1] int32                                  written
+ *   cu_q          [B + 1] int32                              written
+ *   positions     [max_tokens] int32                         written: L + i for row i of a
+ *                 sequence; 0 in rows past the last
+ *   slots         [max_tokens] int32                         written: block * block_size +
+ *                 offset; -1 in rows past the last
+ *   seq_lens_out may be seq_lens and num_free_out num_free; nothing else may
+ *   overlap. A padded batch has max_tokens above the number of new tokens.
+ *
+ * Device checks (ATTN_STATUS_BIT_DEVICE_CHECK): a sequence with a negative
+ * length, more tokens than its table row holds, fewer free blocks than it
+ * needs (it and every later one that needs any), or rows past max_tokens fails:
+ * it gets no block, slots of -1 and a seq_lens_out of -1 - L, which every reader
+ * of the cache refuses (and from which L can be had back; a negative length
+ * stays as it is); cu_q is cut at max_tokens. A free-list or table entry
+ * outside the pool gives a table entry of -1 and slots of -1. num_free outside
+ * [0, free_capacity] counts as 0 and is left as it is.
+ * The result does not depend on scheduling; no atomics touch it.
+ *
+ * Errors (nothing is launched): ATTN_ERR_INVALID_ARG for NULL or misaligned
+ * pointers (positions and slots may be NULL with max_tokens 0) and
+ * non-positive sizes; ATTN_ERR_UNSUPPORTED for B above 8192, or num_blocks *
+ * block_size, max_blocks_per_seq * block_size or B * max_blocks_per_seq of
+ * 2^31 or more; ATTN_ERR_CUDA when the launch fails.
+ */
+ATTN_API int attn_paged_extend(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,
+                               const int32_t* free_blocks, const int32_t* num_free, int32_t* seq_lens_out,
+                               int32_t* num_free_out, int32_t* cu_q, int32_t* positions, int32_t* slots, int B,
+                               int num_blocks, int block_size, int max_blocks_per_seq, int free_capacity,
+                               int max_tokens, int32_t* status, attn_stream_t stream);
+
+/*
+ * attn_paged_release - return the blocks of finished sequences: the
+ * ceil(seq_lens[b] / block_size) entries of every b with finished[b] != 0 go on
+ * top of the free list, in sequence order and then in logical order.
+ *
+ *   seq_lens, num_free       as above                        read
+ *   finished                 [B] int32                       read
+ *   block_table              as above                        read (entries are left as they
+ *                            are: no reader looks past a sequence's length)
+ *   free_blocks              [free_capacity] int32           written from num_free on
+ *   seq_lens_out             [B] int32                       written: 0 for finished sequences
+ *   num_free_out             [1] int32                       written
+ *   In place as for attn_paged_extend.
+ *
+ * The length -1 - L that attn_paged_extend left at a sequence it could not serve
+ * gives back the blocks of L tokens. Device checks: a finished sequence with a
+ * length outside its table row gives back nothing; blocks past free_capacity are dropped; an entry outside the
+ * pool is still put on the list (attn_paged_extend will not hand it out). Each
+ * sets ATTN_STATUS_BIT_DEVICE_CHECK. A block that is on the list already is not
+ * noticed. Errors as for attn_paged_extend.
+ */
+ATTN_API int attn_paged_release(const int32_t* seq_lens, const int32_t* finished, const int32_t* block_table,
+                                int32_t* free_blocks, const int32_t* num_free, int32_t* seq_lens_out,
+                                int32_t* num_free_out, int B, int num_blocks, int block_size, int max_blocks_per_seq,
+                                int free_capacity, int32_t* status, attn_stream_t stream);
+
+/*
+ * attn_qk_norm_rope - RMS norm of every query and key head and the position
+ * rotation, in one pass, from a projection's [B, N, H, d] into the [B, H, N, d]
+ * that attn_prefill reads. V is carried over.
+ *
+ *   y = x / sqrt(mean(x^2) + eps) * weight   (no norm without weights)
+ *   the first rotary_dim elements of y in pairs (a, b), pair f turned by the
+ *   angle of position m: (a cos[m][f] - b sin[m][f], b cos[m][f] + a sin[m][f]).
+ *   Pairs are (f, f + rotary_dim / 2), or (2 f, 2 f + 1) when interleaved != 0;
+ *   elements from rotary_dim on pass through.
+ * Computed in fp32, rounded to bf16 once.
+ *
+ *   q          [B, N, Hq, d] bf16, k, v [B, N, Hkv, d] bf16  read, strided: strides is a HOST
+ *              array of 9 element strides (sequence, token, head) of q, k, v; each a
+ *              multiple of 8; a head row is contiguous. Views of one fused projection do.
+ *   q_weight,
+ *   k_weight   [d] fp32, or bf16 with weight_bf16 != 0       read; both NULL for no norm
+ *   cos_table,
+ *   sin_table  [max_pos, rotary_dim / 2] fp32                read
+ *   positions  [B, N] int32, or NULL for 0 .. N - 1          read
+ *   q_out [B, Hq, N, d], k_out, v_out [B, Hkv, N, d] bf16    written
+ * No output may overlap an input.
+ *
+ * A position outside [0, max_pos) gives NaN rows of q_out and k_out and
+ * ATTN_STATUS_BIT_DEVICE_CHECK.
+ *
+ * Errors (nothing is launched): ATTN_ERR_INVALID_ARG for NULL or misaligned
+ * pointers (16 bytes; positions 4), strides not a multiple of 8, one weight
+ * without the other, a bad size, rotary_dim or eps, max_pos < N without
+ * positions; ATTN_ERR_UNSUPPORTED for d other than 64 or 128, rotary_dim not a
+ * multiple of 16, or B * N * ceil((Hq + 2 Hkv) / 4) of 2^31 or more;
+ * ATTN_ERR_CUDA when the launch fails.
+ */
+ATTN_API int attn_qk_norm_rope(const void* q, const void* k, const void* v, const int64_t* strides,
+                               const void* q_weight, const void* k_weight, int weight_bf16, const float* cos_table,
+                               const float* sin_table, const int32_t* positions, void* q_out, void* k_out,
+                               void* v_out, int B, int N, int Hq, int Hkv, int d, int rotary_dim, int max_pos,
+                               float eps, int interleaved, int32_t* status, attn_stream_t stream);
+
+/*
+ * attn_qk_norm_rope_paged - the serving form: packed tokens, q_out in the
+ * layout of attn_decode_paged and attn_prefill_paged_varlen, K and V appended
+ * to the paged cache in the same pass.
+ *
+ *   q [T, Hq, d], k, v [T, Hkv, d] bf16   read, strided: strides holds (token, head) of q, k, v
+ *   positions   [T] int32                 read
+ *   slots       [T] int32                 read: where the token goes in the cache (block *
+ *               block_size + offset); -1 for none (padding). No slot may come twice.
+ *   q_out       [T, Hq, d] bf16           written
+ *   k_cache,
+ *   v_cache     [num_blocks, block_size, Hkv, d] bf16   the tokens' slots written
+ * Weights, angles, strides and errors as for attn_qk_norm_rope. A position
+ * outside [0, max_pos) gives a NaN row of q_out and no write to the cache, a
+ * slot below -1 or past the pool no write; both set the device-check bit.
+ */
+ATTN_API int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, const int64_t* strides,
+                                     const void* q_weight, const void* k_weight, int weight_bf16,
+                                     const float* cos_table, const float* sin_table, const int32_t* positions,
+                                     const int32_t* slots, void* q_out, void* k_cache, void* v_cache, int T, int Hq,
+                                     int Hkv, int d, int num_blocks, int block_size, int rotary_dim, int max_pos,
+                                     float eps, int interleaved, int32_t* status, attn_stream_t stream);
+
+/*
+ * attn_qk_norm_rope_backward_workspace_bytes - bytes of device workspace
+ * attn_qk_norm_rope_backward needs with weights, on the current device (each
+ * CTA's part of the weight gradients). Returns 0 for invalid sizes.
+ */
+ATTN_API size_t attn_qk_norm_rope_backward_workspace_bytes(int B, int N, int Hq, int Hkv, int d);
+
+/*
+ * attn_qk_norm_rope_backward - gradients of attn_qk_norm_rope.
+ *
+ *   q, k         the forward's inputs (strides: 6, for q and k); NULL without weights
+ *   d_q [B, Hq, N, d], d_k, d_v [B, Hkv, N, d] bf16   read: gradients of the outputs, as
+ *                attn_prefill_backward writes them
+ *   dq [B, N, Hq, d], dk, dv [B, N, Hkv, d] bf16      written, strided by grad_strides (9,
+ *                as for the inputs), so they may be views of one fused gradient
+ *   dq_weight, dk_weight   [d] fp32                   written (with weights)
+ * With dy = R(-m) dz, n = x r, r = 1 / sqrt(mean(x^2) + eps) and g = dy weight:
+ * dx = r (g - n mean(g n)), dweight = sum over rows of dy n. fp32 throughout,
+ * r is computed again from x; the weights' sums have a fixed order, so results
+ * are the same on every run. A position outside [0, max_pos) gives NaN rows
+ * (and weight gradients) and the device-check bit. No output may overlap an
+ * input. Errors as for attn_qk_norm_rope, and ATTN_ERR_WORKSPACE.
+ */
+ATTN_API int attn_qk_norm_rope_backward(const void* q, const void* k, const int64_t* strides, const void* q_weight,
+                                        const void* k_weight, int weight_bf16, const float* cos_table,
+                                        const float* sin_table, const int32_t* positions, const void* d_q,
+                                        const void* d_k, const void* d_v, void* dq, void* dk, void* dv,
+                                        const int64_t* grad_strides, float* dq_weight, float* dk_weight, int B, int N,
+                                        int Hq, int Hkv, int d, int rotary_dim, int max_pos, float eps,
+                                        int interleaved, void* workspace, size_t workspace_bytes, int32_t* status,
+                                        attn_stream_t stream);
 
 /*
  * attn_paged_gather - walk every sequence's block table into a contiguous

@@ -27,7 +27,8 @@ MASKS = {"full": 0, "causal": 1, "window": 2, "sliding_window": 2}
 
 __all__ = ["prefill", "prefill_paged", "decode_paged", "decode_paged_window", "paged_gather", "decode_plan",
            "decode_workspace_bytes", "decode_window_workspace_bytes", "mla_decode_paged", "mla_decode_workspace_bytes",
-           "prefill_backward", "prefill_backward_workspace_bytes", "paged_extend", "paged_release", "qk_norm_rope",
+           "prefill_backward", "prefill_backward_workspace_bytes", "prefill_paged_varlen",
+           "prefill_paged_varlen_workspace_bytes", "paged_extend", "paged_release", "qk_norm_rope",
            "qk_norm_rope_paged", "qk_norm_rope_backward", "qk_norm_rope_backward_workspace_bytes",
            "AttnError", "version"]
 
@@ -440,6 +441,64 @@ def _current() -> int:
 
 def _addr(t) -> int:
     return 0 if t is None else t.data_ptr()
+
+
+def prefill_paged_varlen_workspace_bytes(d: int) -> int:
+    n = int(_lib.lib().attn_prefill_paged_varlen_workspace_bytes(d))
+    if n == 0:
+        raise AttnError(_lib.ATTN_ERR_INVALID_ARG, "attn_prefill_paged_varlen_workspace_bytes")
+    return n
+
+
+@_entry
+def prefill_paged_varlen(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_seq_len: int, mask: str = "causal",
+                         window: int = 0, n_sink: int = 0, sinks=None, scale: float | None = None, out=None, lse=None,
+                         workspace=None, status=None, return_lse: bool = True):
+    """prefill_paged() with each sequence's own number of query rows, packed;
+    returns (O [T, Hq, d], LSE [T, Hq]).
+
+    q [T, Hq, d] bf16; caches [num_blocks, block_size, Hkv, d] bf16;
+    block_table [B, max_blocks] int32; cu_q [B + 1] int32: sequence b has rows
+    [cu_q[b], cu_q[b + 1]), its newest positions; seq_lens [B] int32 counts its
+    cached tokens, the new ones included. window, n_sink and sinks as in
+    decode_paged_window(), with mask="window". Rows outside [cu_q[0], cu_q[B])
+    of a given out and lse stay as they were (else they are undefined). Keyword
+    stream: the CUDA stream (default: the current one).
+    """
+    _need_dims(q, "q", 3, "[T, Hq, d]")
+    _need_dims(k_cache, "k_cache", 4, "[num_blocks, block_size, Hkv, d]")
+    _need_dims(block_table, "block_table", 2, "[B, max_blocks]")
+    dev, bf16, (T, Hq, d), B = q.device, torch.bfloat16, q.shape, block_table.shape[0]
+    num_blocks, block_size, Hkv, _ = pool = k_cache.shape
+    _need_on(q, "q", bf16, (T, Hq, d), dev)
+    _need_on(k_cache, "k_cache", bf16, (num_blocks, block_size, Hkv, d), dev)
+    _need_on(v_cache, "v_cache", bf16, pool, dev)
+    _need_on(block_table, "block_table", torch.int32, block_table.shape, dev)
+    _need_on(cu_q, "cu_q", torch.int32, (B + 1,), dev)
+    _need_on(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    if sinks is not None:
+        _need_on(sinks, "sinks", torch.float32, (Hq,), dev)
+    if mask not in MASKS:
+        raise ValueError(f"mask must be one of {sorted(MASKS)}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    out = _out_on(out, "out", bf16, (T, Hq, d), dev)
+    if lse is not None or return_lse:
+        lse = _out_on(lse, "lse", torch.float32, (T, Hq), dev)
+    _need_status(status, dev)
+    if T == 0:
+        return out, lse
+    if workspace is None:
+        workspace = torch.empty(prefill_paged_varlen_workspace_bytes(d), dtype=torch.uint8, device=dev)
+    _need_workspace(workspace, dev)
+    rc = _lib.lib().attn_prefill_paged_varlen(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                              block_table.data_ptr(), cu_q.data_ptr(), seq_lens.data_ptr(),
+                                              _addr(sinks), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, d, num_blocks,
+                                              block_size, block_table.shape[1], int(max_seq_len), MASKS[mask],
+                                              int(window), int(n_sink), float(scale), workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size(), _addr(status), _current())
+    _lib.check(rc, "attn_prefill_paged_varlen")
+    return out, lse
 
 
 def _table_args(seq_lens, second, second_name, block_table, free_blocks, num_free, seq_lens_out, num_free_out, status):

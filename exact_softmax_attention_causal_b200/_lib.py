@@ -26,6 +26,8 @@ SYMBOLS = (
     "attn_prefill_backward",
     "attn_mla_decode_workspace_bytes",
     "attn_mla_decode_paged",
+    "attn_prefill_paged_varlen_workspace_bytes",
+    "attn_prefill_paged_varlen",
     "attn_paged_extend",
     "attn_paged_release",
     "attn_qk_norm_rope",
@@ -91,6 +93,10 @@ def _declare(lib):
     lib.attn_mla_decode_paged.restype = _i
     lib.attn_paged_gather.argtypes = [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp]
     lib.attn_paged_gather.restype = _i
+    lib.attn_prefill_paged_varlen_workspace_bytes.argtypes = [_i]
+    lib.attn_prefill_paged_varlen_workspace_bytes.restype = _sz
+    lib.attn_prefill_paged_varlen.argtypes = [_vp] * 9 + [_i] * 12 + [_f, _vp, _sz, _vp, _vp]
+    lib.attn_prefill_paged_varlen.restype = _i
     lib.attn_paged_extend.argtypes = [_vp] * 10 + [_i] * 6 + [_vp, _vp]
     lib.attn_paged_extend.restype = _i
     lib.attn_paged_release.argtypes = [_vp] * 7 + [_i] * 5 + [_vp, _vp]

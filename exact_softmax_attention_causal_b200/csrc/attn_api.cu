@@ -119,6 +119,49 @@ int attn_prefill_paged(const void* q, const void* k_cache, const void* v_cache, 
                               reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t attn_prefill_paged_varlen_workspace_bytes(int d) {
+  int sms = 0;
+  if ((d != 64 && d != 128) || current_sm_count(&sms) != ATTN_OK) return 0;
+  return varlen_workspace_bytes(d, sms);
+}
+
+int attn_prefill_paged_varlen(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                              const int32_t* cu_q, const int32_t* seq_lens, const float* sinks, void* o, float* lse,
+                              int B, int T, int Hq, int Hkv, int d, int num_blocks, int block_size,
+                              int max_blocks_per_seq, int max_seq_len, int mask_kind, int window, int n_sink,
+                              float scale, void* workspace, size_t workspace_bytes, int32_t* status,
+                              attn_stream_t stream) {
+  if (!q || !k_cache || !v_cache || !block_table || !cu_q || !seq_lens || !o) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || T <= 0 || Hq <= 0 || Hkv <= 0 || d <= 0 || num_blocks <= 0 || block_size <= 0 ||
+      max_blocks_per_seq <= 0 || max_seq_len <= 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_blocks_per_seq) * block_size < max_seq_len) return ATTN_ERR_INVALID_ARG;
+  if (mask_kind != ATTN_MASK_FULL && mask_kind != ATTN_MASK_CAUSAL && mask_kind != ATTN_MASK_SLIDING_WINDOW)
+    return ATTN_ERR_INVALID_ARG;
+  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < 1) return ATTN_ERR_INVALID_ARG;
+  if (n_sink < 0 || n_sink > max_seq_len || (n_sink > 0 && mask_kind != ATTN_MASK_SLIDING_WINDOW))
+    return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(block_table) || !aligned4(cu_q) || !aligned4(seq_lens) || !aligned4(sinks) || !aligned4(lse))
+    return ATTN_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) return ATTN_ERR_UNSUPPORTED;
+  // row indices are int32; positions leave room for a window's and a tile's width
+  if (static_cast<long long>(T) * Hq > (1LL << 31) - 1 || max_seq_len > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
+  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window >= max_seq_len) mask_kind = ATTN_MASK_CAUSAL, n_sink = 0;
+  int sms = 0;
+  if (current_sm_count(&sms) != ATTN_OK) return ATTN_ERR_CUDA;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < varlen_workspace_bytes(d, sms))
+    return ATTN_ERR_WORKSPACE;
+  const VarlenArgs a{q,           k_cache,    v_cache,   block_table, cu_q,   seq_lens, sinks, o,
+                     lse,         B,          T,         Hq,          Hkv,    d,        num_blocks,
+                     block_size,  max_blocks_per_seq, max_seq_len, mask_kind, window, n_sink, sms,
+                     scale,       workspace,  status};
+  return launch_prefill_varlen(a, reinterpret_cast<cudaStream_t>(stream));
+}
+
 int attn_decode_plan(int B, int Hq, int Hkv, int max_seq_len, int num_sms, int* chunk_tokens, int* num_splits) {
   DecodePlan plan;
   const int rc = plan_decode(B, Hq, Hkv, max_seq_len, num_sms, &plan);

@@ -21,7 +21,7 @@ PKG = os.path.dirname(HERE)
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libattn_b200.so")
 SOURCES = ["attn_api.cu", "prefill_sm100.cu", "decode_sm100.cu", "decode_noalloc.cu", "mla_sm100.cu", "backward_sm100.cu",
-           "paged_tables_sm100.cu", "norm_rope_sm100.cu"]
+           "paged_tables_sm100.cu", "norm_rope_sm100.cu", "prefill_varlen_sm100.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -34,7 +34,7 @@ def nvcc() -> str:
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     srcs = [os.path.join(HERE, s) for s in SOURCES]
-    deps = srcs + [os.path.join(HERE, h) for h in ("ptx.cuh", "internal.h")] + [os.path.join(ROOT, "include", "attn.h")]
+    deps = srcs + [os.path.join(HERE, h) for h in ("ptx.cuh", "internal.h", "prefill_tiles.cuh")] + [os.path.join(ROOT, "include", "attn.h")]
     if not force and os.path.exists(LIB) and all(os.path.getmtime(LIB) >= os.path.getmtime(d) for d in deps):
         return LIB
     cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC",

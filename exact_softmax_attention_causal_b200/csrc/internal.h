@@ -102,6 +102,21 @@ int launch_prefill_paged(const void* q, const void* k_cache, const void* v_cache
                          int num_blocks, int block_size, int max_blocks_per_seq, int max_seq_len, int mask_kind,
                          int window, float scale, int32_t* status, cudaStream_t stream);
 
+// Ragged attention over a paged cache (prefill_varlen_sm100.cu).
+struct VarlenArgs {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *block_table, *cu_q, *seq_lens;
+  const float* sinks;
+  void* o;
+  float* lse;
+  int B, T, Hq, Hkv, d, num_blocks, block_size, max_blocks_per_seq, max_seq_len, mask_kind, window, n_sink, sms;
+  float scale;
+  void* workspace;
+  int32_t* status;
+};
+size_t varlen_workspace_bytes(int d, int sms);
+int launch_prefill_varlen(const VarlenArgs& a, cudaStream_t stream);
+
 // Block tables and slot maps from the requests' lengths (paged_tables_sm100.cu).
 constexpr int kMaxTableSeqs = 8192;  // three 32-bit values per sequence in shared memory
 int launch_paged_extend(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_table,

@@ -1,0 +1,987 @@
+// Ragged attention over a paged cache: sequence b brings its own number n_b of
+// query rows, the newest n_b of its seq_lens[b] cached tokens, packed row after
+// row into one [T, Hq, d] tensor. Chunks of prompts, drafted tokens to verify
+// and single decoded tokens share one launch.
+//
+//   O = softmax(scale * Q K^T + M) V per query head, with key j visible to the
+//   query at position i iff j <= i, and with a window W and n_sink kept
+//   positions iff also i - j < W or j < n_sink; every key without a mask. A
+//   learned sink logit of the head adds exp(sink) to the softmax's sum.
+//
+// Rows. A K/V head's group of query heads shares its keys, so a tile's 128 rows
+// are (token, head of the group) pairs, tpt = 128 / group tokens of them: one
+// decoded token of 4 heads fills 4 rows, a chunk fills whole tiles, and K and V
+// are read once for the whole group. An item is the two tiles (256 rows) of one
+// (sequence, K/V head, stretch of 2 tpt tokens). It streams 128-key tiles.
+//   wide item (more than tpt tokens): both tiles take every key tile;
+//   narrow item: there is one tile of rows, and the two softmax teams take the
+//   even and the odd key tiles with an accumulator each, joined at the end.
+//
+// Split. What the items cost is known only on the GPU and differs by four
+// orders of magnitude within a batch, so the work is dealt by the tile: the
+// items stand in one line, an item as long as its key tiles cost, and CTA c of
+// G takes [W c / G, W (c + 1) / G) of the line's length W. Every CTA finds its
+// stretch by scanning the batch for itself. An item cut by a boundary leaves
+// partial outputs (fp32, unnormalised, with each row's maximum and sum), which
+// a second, small grid joins in a fixed order: nothing depends on timing. A CTA
+// has at most two partials, one per end, so the workspace does not depend on
+// the batch.
+//
+// What bounds it: HBM for narrow items (64 KB of K and V a tile at d = 128,
+// 1.45 us of an SM's share of HBM, against 0.55 us of MMAs), the softmax and the
+// tensor cores for wide ones.
+//
+// Roles, pipeline and the lazily moved maximum are those of the prefill kernel
+// (prefill_sm100.cu): 8 softmax warps, one TMA warp, one MMA warp; probabilities
+// go to the second product as bf16 (the tensor cores take nothing wider at this
+// rate; 2^-9 of each p, averaged over the row), sums and outputs stay in fp32.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "prefill_tiles.cuh"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kVlThreads = 384;
+constexpr int kVlWarps = kVlThreads / 32;
+constexpr int kVlTmaWarp = 8;
+constexpr int kVlMmaWarp = 9;
+constexpr int kVlRows = 2 * kBM;  // rows of an item
+// the register split of the prefill kernel: 256 x 224 + 128 x 56 = 384 x 168
+constexpr uint32_t kVlRegsSoftmax = 224;
+constexpr uint32_t kVlRegsControl = 56;
+static_assert(256 * kVlRegsSoftmax + 128 * kVlRegsControl == kVlThreads * 168, "register split");
+constexpr float kVlRescale = 8.0f;  // base 2: the maximum moves only past this (p <= 2^8)
+// What a key tile costs on the line, and what an item costs besides.
+constexpr int kCostWide = 3, kCostNarrow = 2, kCostItem = 3;
+// A CTA's stretch is at least this long: shorter cuts cost more in joining than they save.
+constexpr int kMinStretch = 4 * kCostWide;
+
+template <int D>
+struct VlCfg {
+  static constexpr int kHalf = 128 * 128;  // bytes of one 64-column box of 128 rows
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kHalves * kHalf;
+  static constexpr int kStages = (D == 128) ? 2 : 4;  // K ring and V ring, each
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kQOff + 2 * kTile;
+  static constexpr int kVOff = kKOff + kStages * kTile;
+  static constexpr int kStageOff = kVOff + kStages * kTile;  // 4 KB per softmax warp
+  static constexpr int kBarOff = kStageOff + 8 * 4096;
+  static constexpr int kBytes = kBarOff + 256;
+  static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 bytes
+  static_assert(kAlloc <= 232448 - 512, "shared memory per CTA (512 bytes are static)");
+  __host__ __device__ static constexpr uint32_t col_s(int x) { return x ? 128u : 0u; }
+  __host__ __device__ static constexpr uint32_t col_o(int x) { return 256u + static_cast<uint32_t>(x * D); }
+};
+
+enum : int {
+  kVbQFull = 0,
+  kVbKFull = 1,
+  kVbVFull = 5,
+  kVbKEmpty = 9,
+  kVbVEmpty = 13,
+  kVbSFull = 17,
+  kVbPLo = 19,
+  kVbPHi = 21,
+  kVbOFinal = 23,
+  kVbDrain = 25,
+  kVbQEmpty = 26,
+};
+
+// An item whose first piece is CTA c's last: what the joining grid needs of it.
+struct VarlenSplit {
+  int pieces;  // 0: CTA c's stretch ends with a whole item
+  int row0, ntok, head0, nheads, wide, pad0, pad1;
+};
+
+struct VarlenParams {
+  __nv_bfloat16* o;
+  float* lse;
+  int32_t* status;
+  const float* sinks;
+  const int32_t* block_table;
+  const int32_t* cu_q;
+  const int32_t* seq_lens;
+  float4* part_o;      // [2 G][d / 4][256]
+  float2* part_ml;     // [2 G][256]
+  VarlenSplit* splits;  // [G]
+  int B, T, Hq, group, gsz, hchunks, tpt, units;  // gsz heads a tile, hchunks tiles a group, units = Hkv * hchunks
+  int row_magic;       // ceil(2^16 / gsz): row * magic >> 16 = row / gsz for rows below 128
+  int mask_kind, window, n_sink, max_blocks, block_size, num_blocks, max_seq_len;
+  float scale_log2;
+  long long budget;
+};
+
+// A sequence's rows and context. bad: lengths that do not fit; it has no items.
+struct VlSeq {
+  int row0, n, nk;
+  bool bad;
+};
+__device__ __forceinline__ VlSeq seq_at(const VarlenParams& p, int b) {
+  const int r0 = __ldg(p.cu_q + b), r1 = __ldg(p.cu_q + b + 1), nk = __ldg(p.seq_lens + b);
+  const bool order = r0 >= 0 && r0 <= r1 && r1 <= p.T;
+  const bool bad = !order || (r1 > r0 && (nk < r1 - r0 || nk > p.max_seq_len));
+  return VlSeq{r0, bad ? 0 : r1 - r0, nk, bad};
+}
+
+// One stretch of rows of a sequence: its tokens, the keys some row sees (the
+// sink positions [0, sink_end) and [key_lo, key_end)), and the T key tiles that
+// hold them: tile j of the list is key tile j, or j + skip behind the sinks'.
+struct VlGeom {
+  int tok0, ntok, pos_lo, key_lo, key_end, sink_end, nst, skip, T;
+  bool wide;
+  __device__ __forceinline__ int key_tile(int j) const { return j < nst ? j : j + skip; }
+  __device__ __forceinline__ int tile_cost() const { return wide ? kCostWide : kCostNarrow; }
+  __device__ __forceinline__ int cost() const { return kCostItem + T * tile_cost(); }
+};
+__device__ __forceinline__ VlGeom geom_at(const VarlenParams& p, int n, int nk, int rt) {
+  VlGeom g;
+  g.tok0 = rt * 2 * p.tpt;
+  g.ntok = min(n - g.tok0, 2 * p.tpt);
+  g.wide = g.ntok > p.tpt;
+  g.pos_lo = nk - n + g.tok0;
+  g.key_end = p.mask_kind == ATTN_MASK_FULL ? nk : g.pos_lo + g.ntok;
+  g.key_lo = p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? max(0, g.pos_lo - p.window + 1) : 0;
+  g.sink_end = min(p.n_sink, g.key_lo);
+  g.nst = (g.sink_end + kBN - 1) / kBN;
+  const int lo = max(g.key_lo / kBN, g.nst);
+  g.skip = lo - g.nst;
+  g.T = g.nst + max(0, (g.key_end - 1) / kBN - lo + 1);
+  return g;
+}
+__device__ __forceinline__ int row_tiles(const VarlenParams& p, int n) { return (n + 2 * p.tpt - 1) / (2 * p.tpt); }
+
+// The cost of one unit (all row tiles for one K/V head) of this lane's
+// sequence; warp-collective, since a long chunk's tiles are summed by all lanes.
+__device__ __forceinline__ long long unit_cost(const VarlenParams& p, const VlSeq& s) {
+  constexpr int kAlone = 8;
+  const int lane = threadIdx.x & 31;
+  const int nrt = row_tiles(p, s.n);
+  long long c = 0;
+  if (nrt <= kAlone)
+    for (int rt = 0; rt < nrt; ++rt) c += geom_at(p, s.n, s.nk, rt).cost();
+  for (unsigned big = __ballot_sync(0xffffffffu, nrt > kAlone); big != 0; big &= big - 1) {
+    const int src = __ffs(big) - 1;
+    const int n = __shfl_sync(0xffffffffu, s.n, src), nk = __shfl_sync(0xffffffffu, s.nk, src);
+    long long part = 0;
+    for (int rt = lane; rt < row_tiles(p, n); rt += 32) part += geom_at(p, n, nk, rt).cost();
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
+    if (lane == src) c = part;
+  }
+  return c;
+}
+
+// CTA c's stretch of the line and where it starts in the batch.
+struct VlPlan {
+  long long start, end, total;
+  int G;
+  int b, u, rt;      // the item that holds `start`
+  long long s;       // where that item starts
+};
+
+// Every role walks the CTA's stretch with its own copy of this.
+struct VlWalk {
+  int b, u, rt, nrt;
+  long long s;
+  VlSeq sq;
+};
+// A piece of an item: key tiles [j0, j1) of its list.
+struct VlPiece {
+  VlGeom g;
+  int j0, j1, b, nk, row0, u;
+  long long x0;  // where the item's first tile stands on the line
+};
+// The next piece of the stretch that has any key tile; false at its end.
+__device__ __forceinline__ bool next_piece(const VarlenParams& p, const VlPlan& pl, VlWalk& w, VlPiece& out) {
+  while (w.s < pl.end) {
+    out.g = geom_at(p, w.sq.n, w.sq.nk, w.rt);
+    out.row0 = w.sq.row0 + out.g.tok0;
+    out.b = w.b;
+    out.nk = w.sq.nk;
+    out.u = w.u;
+    out.x0 = w.s + kCostItem;
+    const int c = out.g.tile_cost();
+    const long long a = pl.start - out.x0, e = pl.end - out.x0;
+    out.j0 = a <= 0 ? 0 : static_cast<int>(min((a + c - 1) / c, static_cast<long long>(out.g.T)));
+    out.j1 = e <= 0 ? 0 : static_cast<int>(min((e + c - 1) / c, static_cast<long long>(out.g.T)));
+    w.s += out.g.cost();
+    if (++w.rt == w.nrt) {
+      w.rt = 0;
+      if (++w.u == p.units) {
+        w.u = 0;
+        if (w.s < pl.end) {  // so a sequence with items follows
+          do w.sq = seq_at(p, ++w.b);
+          while (w.sq.n == 0);
+          w.nrt = row_tiles(p, w.sq.n);
+        }
+      }
+    }
+    if (out.j0 < out.j1) return true;
+  }
+  return false;
+}
+
+// Every (row, key) pair of a tile is visible: rows at positions [qa, qb], keys [k0, k0 + 128).
+__device__ __forceinline__ bool vl_tile_is_full(const VarlenParams& p, int qa, int qb, int k0, int nk) {
+  if (p.mask_kind == ATTN_MASK_FULL) return k0 + kBN <= nk;
+  bool full = k0 + kBN - 1 <= qa;
+  if (p.mask_kind == ATTN_MASK_SLIDING_WINDOW) full = full && (qb - k0 < p.window || k0 + kBN <= p.n_sink);
+  return full;
+}
+
+__device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(kVlThreads, 1)
+    prefill_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vr,
+                          const VarlenParams p) {
+  using C = VlCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long sums_s[kVlWarps];
+  __shared__ VlPlan plan_s;
+  __shared__ volatile int bad_s[4];  // a table entry outside the pool, by item (mod 4)
+  const uint32_t raw_u32 = smem_u32(smem_raw);
+  const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;  // swizzled tiles need 1024-byte alignment
+  uint8_t* smem = smem_raw + (sbase - raw_u32);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+
+  // the joining grid may be set up now; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+  const uint32_t bars = sbase + C::kBarOff;
+  auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 224);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 228);
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(kVbQFull), 1);
+    mbar_init(bar(kVbQEmpty), 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(kVbKFull + s), 1);
+      mbar_init(bar(kVbVFull + s), 1);
+      mbar_init(bar(kVbKEmpty + s), 1);
+      mbar_init(bar(kVbVEmpty + s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(kVbSFull + x), 1);
+      mbar_init(bar(kVbPLo + x), kBM);
+      mbar_init(bar(kVbPHi + x), kBM);
+      mbar_init(bar(kVbOFinal + x), 1);
+    }
+    mbar_init(bar(kVbDrain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    p.splits[cta].pieces = 0;
+  }
+  if (warp == kVlMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+
+  // ---- the line: total length, then the item at this CTA's start. Warp w takes
+  // sequences [32 (12 r + w), + 32) in round r; costs of one round stay in registers.
+  {
+    const int rounds = (p.B + kVlThreads - 1) / kVlThreads;
+    VlSeq sq{0, 0, 0, false};
+    long long uc = 0, sum = 0;
+    for (int r = 0; r < rounds; ++r) {
+      const int b = r * kVlThreads + static_cast<int>(threadIdx.x);
+      sq = b < p.B ? seq_at(p, b) : VlSeq{0, 0, 0, false};
+      uc = unit_cost(p, sq);
+      sum += uc * p.units;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) sums_s[warp] = sum;
+    __syncthreads();
+    long long total = 0;
+    for (int w = 0; w < kVlWarps; ++w) total += sums_s[w];
+    const long long most = total / kMinStretch;
+    const int G = most < 1 ? 1 : (most < gridDim.x ? static_cast<int>(most) : static_cast<int>(gridDim.x));
+    const long long start = cta < G ? total * cta / G : 0, end = cta < G ? total * (cta + 1) / G : 0;
+    long long before = 0;  // of all earlier rounds
+    for (int r = 0; r < rounds; ++r) {
+      const int b = r * kVlThreads + static_cast<int>(threadIdx.x);
+      if (rounds > 1) {
+        sq = b < p.B ? seq_at(p, b) : VlSeq{0, 0, 0, false};
+        uc = unit_cost(p, sq);
+      }
+      const long long c = uc * p.units;
+      long long inc = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      __syncthreads();  // sums_s has been read
+      if (lane == 31) sums_s[warp] = inc;
+      __syncthreads();
+      long long mine = before;
+      for (int w = 0; w < kVlWarps; ++w) {
+        if (w < warp) mine += sums_s[w];
+        before += sums_s[w];
+      }
+      mine += inc - c;
+      if (c > 0 && start < end && mine <= start && start < mine + c) {
+        long long off = start - mine;
+        const int u = static_cast<int>(off / uc);
+        off -= u * uc;
+        long long at = 0;
+        int rt = 0;
+        for (;; ++rt) {
+          const int ic = geom_at(p, sq.n, sq.nk, rt).cost();
+          if (off < at + ic) break;
+          at += ic;
+        }
+        plan_s.b = b;
+        plan_s.u = u;
+        plan_s.rt = rt;
+        plan_s.s = start - (off - at);
+      }
+    }
+    if (threadIdx.x == 0) {
+      plan_s.start = start;
+      plan_s.end = end;
+      plan_s.total = total;
+      plan_s.G = G;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long budget = p.budget;
+  const VlPlan& pl = plan_s;
+  auto first_walk = [&]() -> VlWalk {
+    VlWalk w;
+    w.s = pl.start < pl.end ? pl.s : pl.end;
+    w.b = w.u = w.rt = w.nrt = 0;
+    w.sq = VlSeq{0, 0, 0, false};
+    if (pl.start < pl.end) {
+      w.b = pl.b;
+      w.u = pl.u;
+      w.rt = pl.rt;
+      w.sq = seq_at(p, w.b);
+      w.nrt = row_tiles(p, w.sq.n);
+    }
+    return w;
+  };
+
+  if (warp >= kVlTmaWarp) {
+    regs_dec<kVlRegsControl>();
+    if (warp == kVlTmaWarp) {
+      // ---------------------------------------------------------- TMA producer
+      // Lane 0 waits on the ring and arms the barriers, lane e copies block e of a
+      // key tile. A block that no row of the item sees, that lies past the sequence
+      // or whose entry is outside the pool is asked for at block num_blocks, which
+      // TMA fills with zeros: nothing is read of it, its keys are masked, and its
+      // probabilities of 0 meet zeros in V. In the block where the sequence ends, V
+      // goes row by row (all lanes), zeros behind the end, for the same reason: 0
+      // times what a pool holds there could be NaN. K's rows there are masked.
+      if (lane == 0) {
+        prefetch_tmap(&tm_q);
+        prefetch_tmap(&tm_k);
+        prefetch_tmap(&tm_v);
+      }
+      const int bs = p.block_size, boxes = kBN / bs;
+      VlWalk w = first_walk();
+      VlPiece pc;
+      int g = 0, k_issued = 0, v_issued = 0, it = 0;
+      bool ok = true;
+      while (ok && next_piece(p, pl, w, pc)) {
+        const VlGeom& gm = pc.g;
+        const int nt = pc.j1 - pc.j0;
+        const int kvh = pc.u / p.hchunks, hc = pc.u - kvh * p.hchunks;
+        const int flag = it & 3;
+        if (lane == 0) bad_s[flag] = 0;
+        __syncwarp();
+        auto fetch = [&](int j) -> int {
+          const int key = gm.key_tile(pc.j0 + j) * kBN + lane * bs;
+          const bool seen = lane < boxes && key < gm.key_end && (key + bs > gm.key_lo || key < gm.sink_end);
+          int ent = p.num_blocks;
+          if (seen) {
+            ent = __ldg(p.block_table + static_cast<size_t>(pc.b) * p.max_blocks + key / bs);
+            if (ent < 0 || ent >= p.num_blocks) {
+              ent = p.num_blocks;
+              bad_s[flag] = 1;
+            }
+          }
+          __syncwarp();
+          return ent;
+        };
+        auto load_k = [&](uint32_t dst, uint32_t full, int ent) {
+          if (lane < boxes)
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              tma_load_4d(dst + lane * bs * 128 + hh * C::kHalf, &tm_k, full, hh * 64, kvh, 0, ent);
+        };
+        auto load_v = [&](uint32_t dst, uint32_t full, int j, int ent) {
+          const int key = gm.key_tile(pc.j0 + j) * kBN + lane * bs;
+          const bool part = lane < boxes && key < pc.nk && key + bs > pc.nk && ent != p.num_blocks;
+          if (lane < boxes && !part)
+            for (int hh = 0; hh < C::kHalves; ++hh)
+              tma_load_4d(dst + lane * bs * 128 + hh * C::kHalf, &tm_v, full, hh * 64, kvh, 0, ent);
+          const unsigned who = __ballot_sync(0xffffffffu, part);
+          if (who != 0) {
+            const int src = __ffs(who) - 1;
+            const int phys = __shfl_sync(0xffffffffu, ent, src);
+            const int valid = pc.nk - __shfl_sync(0xffffffffu, key, src);  // 1 .. bs - 1 rows hold tokens
+            for (int i = lane; i < bs * C::kHalves; i += 32) {
+              const int slot = i / C::kHalves, hh = i - slot * C::kHalves;
+              tma_load_4d(dst + (src * bs + slot) * 128 + hh * C::kHalf, &tm_vr, full, hh * 64, kvh, slot,
+                          slot < valid ? phys : p.num_blocks);
+            }
+          }
+        };
+        int ent_k = fetch(0), ent_v = p.num_blocks;
+        bool armed = true;
+        if (lane == 0) {
+          armed = (it == 0) || mbar_wait_bounded(bar(kVbQEmpty), (it - 1) & 1, budget, abort_flag);
+          if (armed) {
+            const int tiles = gm.wide ? 2 : 1;
+            mbar_arrive_expect_tx(bar(kVbQFull), tiles * C::kHalves * p.gsz * p.tpt * 128);
+            for (int x = 0; x < tiles; ++x)
+              for (int hh = 0; hh < C::kHalves; ++hh)
+                tma_load_3d(sbase + C::kQOff + x * C::kTile + hh * C::kHalf, &tm_q, bar(kVbQFull), hh * 64,
+                            kvh * p.group + hc * p.gsz, pc.row0 + x * p.tpt);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, armed, 0);
+        if (!ok) break;
+        ++it;
+        for (int i = 0; i <= nt; ++i) {
+          if (i < nt) {
+            const int gi = g + i, s = gi % C::kStages, rnd = gi / C::kStages;
+            if (lane == 0) {
+              armed = (rnd == 0) || mbar_wait_bounded(bar(kVbKEmpty + s), (rnd - 1) & 1, budget, abort_flag);
+              if (armed) mbar_arrive_expect_tx(bar(kVbKFull + s), C::kTile);
+            }
+            ok = __shfl_sync(0xffffffffu, armed, 0);
+            if (!ok) break;
+            load_k(sbase + C::kKOff + s * C::kTile, bar(kVbKFull + s), ent_k);
+            k_issued = gi + 1;
+          }
+          if (i >= 1) {
+            const int gv = g + i - 1, s = gv % C::kStages, rnd = gv / C::kStages;
+            if (lane == 0) {
+              armed = (rnd == 0) || mbar_wait_bounded(bar(kVbVEmpty + s), (rnd - 1) & 1, budget, abort_flag);
+              if (armed) mbar_arrive_expect_tx(bar(kVbVFull + s), C::kTile);
+            }
+            ok = __shfl_sync(0xffffffffu, armed, 0);
+            if (!ok) break;
+            load_v(sbase + C::kVOff + s * C::kTile, bar(kVbVFull + s), i - 1, ent_v);
+            v_issued = gv + 1;
+          }
+          ent_v = ent_k;
+          if (i + 1 < nt) ent_k = fetch(i + 1);
+        }
+        g += nt;
+      }
+      if (lane == 0) {
+        if (!ok) raise_abort(abort_flag, p.status);
+        // Drain: the newest copy of every stage and of Q has landed before the CTA may exit.
+        volatile int never = 0;
+        if (it > 0) mbar_wait_bounded(bar(kVbQFull), (it - 1) & 1, kDrainBudgetCycles, &never);
+        for (int j = (k_issued > C::kStages ? k_issued - C::kStages : 0); j < k_issued; ++j)
+          mbar_wait_bounded(bar(kVbKFull + j % C::kStages), (j / C::kStages) & 1, kDrainBudgetCycles, &never);
+        for (int j = (v_issued > C::kStages ? v_issued - C::kStages : 0); j < v_issued; ++j)
+          mbar_wait_bounded(bar(kVbVFull + j % C::kStages), (j / C::kStages) & 1, kDrainBudgetCycles, &never);
+      }
+    } else if (warp == kVlMmaWarp && lane == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const uint64_t dq0 = desc_sw128(sbase + C::kQOff, 16, 1024);
+      const uint64_t dk0 = desc_sw128(sbase + C::kKOff, 16, 1024);
+      const uint64_t dv0 = desc_sw128(sbase + C::kVOff, C::kHalf, 1024);
+      constexpr uint64_t kTileUnits = C::kTile >> 4;
+      auto wait_k = [&](int g) -> bool {
+        const bool r = mbar_wait_bounded(bar(kVbKFull + g % C::kStages), (g / C::kStages) & 1, budget, abort_flag);
+        tc_fence_after();
+        return r;
+      };
+      // team x's scores of key tile g (counted over the CTA's stretch) with Q tile qx
+      auto issue_s = [&](int x, int qx, int g) {
+        mma_scores<D>(tmem + C::col_s(x), dq0 + static_cast<uint64_t>(qx) * kTileUnits,
+                      dk0 + static_cast<uint64_t>(g % C::kStages) * kTileUnits);
+        tc_commit(bar(kVbSFull + x));
+      };
+      int cnt[2] = {0, 0};  // score tiles of each team so far
+      // O_x (+)= P_x V, each half of P as it lands
+      auto pv = [&](int x, int g, bool first) -> bool {
+        const uint64_t dv = dv0 + static_cast<uint64_t>(g % C::kStages) * kTileUnits;
+        if (!mbar_wait_bounded(bar(kVbPLo + x), cnt[x] & 1, budget, abort_flag)) return false;
+        tc_fence_after();
+        mma_pv<D, 0, 4>(tmem + C::col_o(x), tmem + C::col_s(x), dv, first);
+        if (!mbar_wait_bounded(bar(kVbPHi + x), cnt[x] & 1, budget, abort_flag)) return false;
+        tc_fence_after();
+        mma_pv<D, 4, 8>(tmem + C::col_o(x), tmem + C::col_s(x), dv, first);
+        ++cnt[x];
+        return true;
+      };
+      VlWalk w = first_walk();
+      VlPiece pc;
+      int g = 0, it = 0;
+      bool ok = true;
+      while (ok && next_piece(p, pl, w, pc)) {
+        const int nt = pc.j1 - pc.j0;
+        const bool wide = pc.g.wide;
+        const int teams = wide ? 2 : 1, ahead = wide ? 1 : 2;  // key tiles a score runs ahead of its P V
+        if (!mbar_wait_bounded(bar(kVbQFull), it & 1, budget, abort_flag)) {
+          ok = false;
+          break;
+        }
+        // the first scores of both teams
+        for (int j = 0; j < min(ahead, nt) && ok; ++j) {
+          if (!wait_k(g + j)) {
+            ok = false;
+            break;
+          }
+          if (wide) {
+            issue_s(0, 0, g);
+            issue_s(1, 1, g);
+          } else {
+            issue_s(j, 0, g + j);
+          }
+          tc_commit(bar(kVbKEmpty + (g + j) % C::kStages));
+          if (j == nt - 1) tc_commit(bar(kVbQEmpty));
+        }
+        for (int j = 0; j < nt && ok; ++j) {
+          const int gj = g + j, s = gj % C::kStages, jn = j + ahead;
+          if (!mbar_wait_bounded(bar(kVbVFull + s), (gj / C::kStages) & 1, budget, abort_flag)) {
+            ok = false;
+            break;
+          }
+          for (int t = 0; t < teams && ok; ++t) {
+            const int x = wide ? t : (j & 1);
+            // P V of key tile j, then (in issue order, so they overwrite P only after it is
+            // read) this team's next scores
+            if (!pv(x, gj, wide ? j == 0 : j < 2)) {
+              ok = false;
+              break;
+            }
+            if (jn >= nt) tc_commit(bar(kVbOFinal + x));
+            if (t == teams - 1) tc_commit(bar(kVbVEmpty + s));
+            if (jn < nt) {
+              if (t == 0 && !wait_k(g + jn)) {
+                ok = false;
+                break;
+              }
+              issue_s(x, wide ? t : 0, g + jn);
+              if (t == teams - 1) {
+                tc_commit(bar(kVbKEmpty + (g + jn) % C::kStages));
+                if (jn == nt - 1) tc_commit(bar(kVbQEmpty));  // that was the item's last read of Q
+              }
+            }
+          }
+        }
+        g += nt;
+        ++it;
+      }
+      if (!ok) raise_abort(abort_flag, p.status);
+      // Drain: every MMA this thread issued has completed before TMEM is freed.
+      tc_commit(bar(kVbDrain));
+      volatile int never = 0;
+      mbar_wait_bounded(bar(kVbDrain), 0, kDrainBudgetCycles, &never);
+    } else if (warp > kVlMmaWarp) {
+      // ---------------------------------------------------------- rows of sequences that have no valid lengths
+      for (int b = cta; b < p.B; b += gridDim.x) {
+        const VlSeq sq = seq_at(p, b);
+        if (!sq.bad) continue;
+        const int t = threadIdx.x - 32 * (kVlMmaWarp + 1);
+        if (t == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
+        const int r0 = max(0, sq.row0), r1 = min(p.T, __ldg(p.cu_q + b + 1));
+        for (int r = r0; r < r1; ++r) {
+          __nv_bfloat16* row = p.o + static_cast<size_t>(r) * p.Hq * D;
+          for (int i = t; i < p.Hq * D / 8; i += 64)
+            reinterpret_cast<uint4*>(row)[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+          if (p.lse != nullptr)
+            for (int i = t; i < p.Hq; i += 64) p.lse[static_cast<size_t>(r) * p.Hq + i] = NAN;
+        }
+      }
+    }
+  } else {
+    regs_inc<kVlRegsSoftmax>();
+    // ------------------------------------------------------------ softmax teams (warps 0-3, 4-7)
+    const int x = warp >> 2;
+    const int r = threadIdx.x & (kBM - 1);  // row of the tile = TMEM lane
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t colS = lane_base + C::col_s(x);
+    const uint32_t colO = lane_base + C::col_o(x);
+    const float sl2 = p.scale_log2;
+    const int rtok = (r * p.row_magic) >> 16, rhead = r - rtok * p.gsz;  // this row's token and head in a tile
+    VlWalk w = first_walk();
+    VlPiece pc;
+    int cnt = 0, fin = 0, it = 0;  // this team's score tiles, finished outputs; items
+    bool ok = true;
+    for (; next_piece(p, pl, w, pc); ++it) {
+      const VlGeom& gm = pc.g;
+      const int nt = pc.j1 - pc.j0;
+      const bool wide = gm.wide;
+      const int kvh = pc.u / p.hchunks, hc = pc.u - kvh * p.hchunks;
+      const int head0 = kvh * p.group + hc * p.gsz, nheads = min(p.gsz, p.group - hc * p.gsz);
+      const int t0 = wide ? x * p.tpt : 0;                 // the tile's first token in the item
+      const int ntok = min(gm.ntok - t0, p.tpt);           // and its tokens (a wide item's second tile has some)
+      const int qa = gm.pos_lo + t0, qpos = qa + rtok;
+      const bool row_valid = rtok < ntok && rhead < nheads;
+      const bool active = (warp & 3) * 32 < ntok * p.gsz;  // the warp has rows of the item
+      float m_used = -INFINITY;  // max the exponentials are taken against (base 2)
+      float l_sum = 0.f;         // running sum of 2^(s - m_used)
+      for (int j = wide ? 0 : x; j < nt && ok; j += wide ? 1 : 2, ++cnt) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kVbSFull + x), cnt & 1, budget, abort_flag));
+        if (!ok) break;
+        if (!active) {  // rows nobody reads: whatever P holds there is fine
+          mbar_arrive(bar(kVbPLo + x));
+          mbar_arrive(bar(kVbPHi + x));
+          continue;
+        }
+        const int k0 = gm.key_tile(pc.j0 + j) * kBN;
+        tc_fence_after();
+        uint32_t raw[kBN];
+#pragma unroll
+        for (int c = 0; c < kBN / 32; ++c)
+          tmem_ld_32x32b_x32(colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[c * 32]));
+        tc_wait_ld();
+        float sv[kBN];
+#pragma unroll
+        for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(raw[c]);
+        if (!vl_tile_is_full(p, qa, qa + ntok - 1, k0, pc.nk)) {
+          // visible keys of this row: columns [cmin, cmax], and those before csink
+          const int cmax = (p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : qpos) - k0;
+          const int cmin = p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? qpos - k0 - p.window + 1 : 0;
+          const int csink = p.n_sink - k0;
+#pragma unroll
+          for (int c = 0; c < kBN; ++c) sv[c] = ((c >= cmin || c < csink) && c <= cmax) ? sv[c] : -INFINITY;
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kBN; c += 8) {
+          mx0 = max3f(mx0, sv[c], sv[c + 1]);
+          mx1 = max3f(mx1, sv[c + 2], sv[c + 3]);
+          mx2 = max3f(mx2, sv[c + 4], sv[c + 5]);
+          mx3 = max3f(mx3, sv[c + 6], sv[c + 7]);
+        }
+        const float m_new = fmaxf(m_used, max3f(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
+        bool rescale_o = false;
+        float factor = 1.f;
+        if (m_new > m_used + kVlRescale) {  // also true for the first visible key (m_used = -inf)
+          const bool prev_finite = (m_used != -INFINITY);
+          factor = prev_finite ? fast_exp2(m_used - m_new) : 0.f;
+          l_sum *= factor;
+          rescale_o = prev_finite;
+          m_used = m_new;
+        }
+        // The score barrier was committed after this team's previous P V: O is stable.
+        if (__any_sync(0xffffffffu, rescale_o)) rescale_row_t<D>(colO, rescale_o ? factor : 1.f);
+        // a row with nothing visible yet uses m = 0
+        const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
+#pragma unroll
+        for (int cc = 0; cc < kBN / 32; ++cc) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int c = cc * 32 + 2 * e;
+            const float2 xv =
+                ffma2(make_float2(sv[c], sv[c + 1]), make_float2(sl2, sl2), make_float2(neg_m, neg_m));
+            float2 pv;
+            pv.x = fast_exp2(xv.x);
+            pv.y = fast_exp2(xv.y);
+            float2& acc = (e & 3) == 0 ? acc0 : (e & 3) == 1 ? acc1 : (e & 3) == 2 ? acc2 : acc3;
+            acc = fadd2(acc, pv);
+            pk[e] = pack_bf16x2(pv.x, pv.y);
+          }
+          tmem_st_32x32b_x16(colS + cc * 16, pk);  // over score columns already consumed
+          if (cc == 1 || cc == 3) {
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar((cc == 1 ? kVbPLo : kVbPHi) + x));
+          }
+        }
+        l_sum += ((acc0.x + acc0.y) + (acc1.x + acc1.y)) + ((acc2.x + acc2.y) + (acc3.x + acc3.y));
+      }
+      const bool took_part = wide || nt > x;
+      if (ok && took_part)
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kVbOFinal + x), fin & 1, budget, abort_flag));
+      if (took_part) ++fin;
+      if (!ok) raise_abort(abort_flag, p.status);
+      tc_fence_after();
+      if (!active || !took_part) {
+        tc_fence_before();
+        continue;
+      }
+
+      // ---- the two teams of a narrow item are joined: both know both sums, team 1
+      // hands its output over in 32-column pieces through its staging box
+      const bool join = !wide && nt > 1;
+      const uint32_t stage = sbase + C::kStageOff + warp * 4096;
+      float f = 1.f;
+      if (join) {
+        float2* mine = reinterpret_cast<float2*>(smem + C::kStageOff + warp * 4096);
+        mine[lane] = make_float2(m_used, l_sum);
+        pair_barrier(1 + (warp & 3));
+        const float2 other = reinterpret_cast<float2*>(smem + C::kStageOff + (warp ^ 4) * 4096)[lane];
+        pair_barrier(1 + (warp & 3));  // read before the boxes are written again
+        const float m = fmaxf(m_used, other.x);
+        f = m_used == -INFINITY ? 0.f : exp2f(m_used - m);
+        l_sum = l_sum * f + (other.x == -INFINITY ? 0.f : other.y * exp2f(other.x - m));
+        m_used = m;
+      }
+      if (join && x == 1) {
+        float* box = reinterpret_cast<float*>(smem + C::kStageOff + warp * 4096);
+#pragma unroll
+        for (int c32 = 0; c32 < D / 32; ++c32) {
+          uint32_t ov[32];
+          if (ok) {
+            tmem_ld_32x32b_x32(colO + c32 * 32, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) box[e * 32 + lane] = f == 0.f ? 0.f : __uint_as_float(ov[e]) * f;
+          }
+          pair_barrier(1 + (warp & 3));
+          pair_barrier(1 + (warp & 3));
+        }
+        tc_fence_before();
+        continue;
+      }
+
+      const bool whole = pc.j0 == 0 && pc.j1 == gm.T;
+      const bool out_ok = ok && bad_s[it & 3] == 0;
+      if (!out_ok && ok && lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
+      const int slot = cta * 2 + (pc.j0 == 0 ? 1 : 0);
+      float norm = 1.f;
+      if (whole) {
+        float m = m_used, l = l_sum, ff = 1.f;
+        if (p.sinks != nullptr && row_valid) {  // one more column with no value
+          const float sk = __ldg(p.sinks + head0 + rhead) * kLog2e;
+          m = fmaxf(m_used, sk);
+          ff = exp2f(m_used - m);
+          l = l * ff + exp2f(sk - m);
+        }
+        norm = out_ok ? ff / l : NAN;
+        if (row_valid && p.lse != nullptr)
+          p.lse[static_cast<size_t>(pc.row0 + t0 + rtok) * p.Hq + head0 + rhead] = out_ok ? (m + log2f(l)) * kLn2 : NAN;
+      } else {
+        p.part_ml[static_cast<size_t>(slot) * kVlRows + x * kBM + r] = make_float2(m_used, out_ok ? l_sum : NAN);
+        if (pc.j0 == 0 && threadIdx.x == 0) {
+          // the CTA that holds the item's last tile, by the line's arithmetic
+          const long long last = pc.x0 + static_cast<long long>(gm.T - 1) * gm.tile_cost();
+          const int c1 = static_cast<int>(((last + 1) * pl.G - 1) / pl.total);
+          p.splits[cta] = VarlenSplit{c1 - cta + 1, pc.row0, gm.ntok, head0, nheads, wide ? 1 : 0, 0, 0};
+        }
+      }
+      const float* box = reinterpret_cast<const float*>(smem + C::kStageOff + (warp + 4) * 4096);
+#pragma unroll
+      for (int hh = 0; hh < D / 64; ++hh) {
+#pragma unroll
+        for (int q32 = 0; q32 < 2; ++q32) {
+          uint32_t ov[32];
+          if (ok) {
+            tmem_ld_32x32b_x32(colO + hh * 64 + q32 * 32, ov);
+            tc_wait_ld();
+          }
+          if (join) {
+            pair_barrier(1 + (warp & 3));
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              ov[e] = __float_as_uint((f == 0.f ? 0.f : __uint_as_float(ov[e]) * f) + box[e * 32 + lane]);
+            pair_barrier(1 + (warp & 3));
+          }
+          if (whole) {
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+              uint32_t w4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float a0 = ok ? __uint_as_float(ov[c4 * 8 + 2 * e]) * norm : NAN;
+                const float a1 = ok ? __uint_as_float(ov[c4 * 8 + 2 * e + 1]) * norm : NAN;
+                w4[e] = pack_bf16x2(a0, a1);
+              }
+              const uint32_t dst = stage + lane * 128 + (((q32 * 4 + c4) ^ (lane & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst), "r"(w4[0]), "r"(w4[1]), "r"(w4[2]),
+                           "r"(w4[3])
+                           : "memory");
+            }
+          } else {
+#pragma unroll
+            for (int c4 = 0; c4 < 8; ++c4) {
+              const float4 v = ok ? make_float4(__uint_as_float(ov[4 * c4]), __uint_as_float(ov[4 * c4 + 1]),
+                                                __uint_as_float(ov[4 * c4 + 2]), __uint_as_float(ov[4 * c4 + 3]))
+                                  : make_float4(NAN, NAN, NAN, NAN);
+              p.part_o[(static_cast<size_t>(slot) * (D / 4) + hh * 16 + q32 * 8 + c4) * kVlRows + x * kBM + r] = v;
+            }
+          }
+        }
+        if (whole) {  // 8 lanes a row, 16 bytes each; only rows of this sequence and these heads
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int wr = i * 4 + (lane >> 3), c = lane & 7;
+            const int row = (warp & 3) * 32 + wr;
+            const int tk = (row * p.row_magic) >> 16, hd = row - tk * p.gsz;
+            if (tk < ntok && hd < nheads) {
+              uint4 v;
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                           : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                           : "r"(stage + wr * 128 + ((c ^ (wr & 7)) << 4)));
+              __nv_bfloat16* dst =
+                  p.o + (static_cast<size_t>(pc.row0 + t0 + tk) * p.Hq + head0 + hd) * D + hh * 64;
+              reinterpret_cast<uint4*>(dst)[c] = v;
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // The next item's first P V overwrites O: its P is announced only after
+      // these loads completed (tcgen05.wait::ld above, fence before the arrive).
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kVlMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the pieces of the item that CTA blockIdx.x of the grid above started
+// and did not finish: out = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), in
+// the order of the pieces. A thread takes 4 columns of a row.
+constexpr int kJoinThreads = 256, kJoinParts = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) prefill_varlen_join_kernel(const VarlenParams p) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the other grid has finished and its stores are visible
+  const int c = blockIdx.x;
+  const VarlenSplit sp = p.splits[c];
+  if (sp.pieces == 0) return;
+  // rows in use, in whole warps: the first tile's, or both tiles
+  const int nr = sp.wide ? kVlRows : (min(sp.ntok, p.tpt) * p.gsz + 31) & ~31;
+  for (int i = blockIdx.y * kJoinThreads + threadIdx.x; i < nr * (D / 4); i += kJoinParts * kJoinThreads) {
+    const int c4 = i / nr, row = i - c4 * nr;
+    const int r = row & (kBM - 1);
+    const int tk = (r * p.row_magic) >> 16, hd = r - tk * p.gsz;
+    const int tok = (row >> 7) * p.tpt + tk;
+    if (tk >= p.tpt || tok >= sp.ntok || hd >= sp.nheads) continue;
+    const float sk = p.sinks != nullptr ? __ldg(p.sinks + sp.head0 + hd) * kLog2e : -INFINITY;
+    float m = sk;
+#pragma unroll 4
+    for (int k = 0; k < sp.pieces; ++k) m = fmaxf(m, p.part_ml[static_cast<size_t>(2 * (c + k) + (k == 0)) * kVlRows + row].x);
+    float l = p.sinks != nullptr ? exp2f(sk - m) : 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < sp.pieces; ++k) {
+      const size_t slot = 2 * (c + k) + (k == 0);
+      const float2 ml = p.part_ml[slot * kVlRows + row];
+      const float4 v = p.part_o[(slot * (D / 4) + c4) * kVlRows + row];
+      // a piece in which this row sees nothing has the maximum -inf, the sum 0 and the output 0
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
+      l += ml.y * f;
+      acc.x += v.x * f;
+      acc.y += v.y * f;
+      acc.z += v.z * f;
+      acc.w += v.w * f;
+    }
+    const float inv = 1.f / l;
+    const size_t out = static_cast<size_t>(sp.row0 + tok) * p.Hq + sp.head0 + hd;
+    *reinterpret_cast<uint2*>(p.o + out * D + 4 * c4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (c4 == 0 && p.lse != nullptr) p.lse[out] = (m + log2f(l)) * kLn2;
+  }
+}
+
+// Packed queries [T, Hq, d] as a rank-3 tensor; box = 64 columns x heads x tokens.
+bool encode_packed_q(CUtensorMap* map, const void* base, int d, int hq, int tokens, int box_heads, int box_tokens) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hq),
+                              static_cast<cuuint64_t>(tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(hq) * d * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t estride[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                         estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch_varlen_t(const VarlenArgs& a, cudaStream_t stream) {
+  VarlenParams p{};
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.status = a.status;
+  p.sinks = a.sinks;
+  p.block_table = a.block_table;
+  p.cu_q = a.cu_q;
+  p.seq_lens = a.seq_lens;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.part_o = reinterpret_cast<float4*>(ws);
+  ws += static_cast<size_t>(2 * a.sms) * kVlRows * D * sizeof(float);
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  ws += static_cast<size_t>(2 * a.sms) * kVlRows * sizeof(float2);
+  p.splits = reinterpret_cast<VarlenSplit*>(ws);
+  p.B = a.B;
+  p.T = a.T;
+  p.Hq = a.Hq;
+  p.group = a.Hq / a.Hkv;
+  p.gsz = p.group < kBM ? p.group : kBM;
+  p.hchunks = (p.group + p.gsz - 1) / p.gsz;
+  p.tpt = kBM / p.gsz;
+  p.units = a.Hkv * p.hchunks;
+  p.row_magic = (65536 + p.gsz - 1) / p.gsz;
+  p.mask_kind = a.mask_kind;
+  p.window = a.window;
+  p.n_sink = a.n_sink;
+  p.max_blocks = a.max_blocks_per_seq;
+  p.block_size = a.block_size;
+  p.num_blocks = a.num_blocks;
+  p.max_seq_len = a.max_seq_len;
+  p.scale_log2 = a.scale * kLog2e;
+  p.budget = wait_budget_cycles();
+  CUtensorMap tq, tk, tv, tvr;
+  if (!encode_packed_q(&tq, a.q, D, a.Hq, a.T, p.gsz, p.tpt) ||
+      !encode_pool(&tk, a.k_cache, D, a.Hkv, a.block_size, a.num_blocks, a.block_size) ||
+      !encode_pool(&tv, a.v_cache, D, a.Hkv, a.block_size, a.num_blocks, a.block_size) ||
+      !encode_pool(&tvr, a.v_cache, D, a.Hkv, a.block_size, a.num_blocks, 1))
+    return ATTN_ERR_CUDA;
+  constexpr int smem = VlCfg<D>::kAlloc;
+  if (cudaFuncSetAttribute(prefill_varlen_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  prefill_varlen_kernel<D><<<a.sms, kVlThreads, smem, stream>>>(tq, tk, tv, tvr, p);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.sms, kJoinParts);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_varlen_join_kernel<D>, p) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t varlen_workspace_bytes(int d, int sms) {
+  return static_cast<size_t>(2 * sms) * kVlRows * (d * sizeof(float) + sizeof(float2)) + sms * sizeof(VarlenSplit);
+}
+
+int launch_prefill_varlen(const VarlenArgs& a, cudaStream_t stream) {
+  return a.d == 128 ? launch_varlen_t<128>(a, stream) : launch_varlen_t<64>(a, stream);
+}
+
+}  // namespace attn

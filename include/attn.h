@@ -27,6 +27,9 @@
  *   attn_mla_decode_paged - absorbed Multi-head Latent Attention decode over a
  *                        paged latent cache ("Modern Attention Mechanisms",
  *                        section 7; "Module 09", the MLA section).
+ *   attn_prefill_paged_varlen - the same with each sequence's own number of
+ *                        query rows, packed: prompt chunks, drafted tokens and
+ *                        single decoded tokens in one call.
  *   attn_paged_extend, attn_paged_release - block tables, positions and slot
  *                        maps built on the GPU from the requests' lengths.
  *   attn_qk_norm_rope (and _backward, _paged) - query and key norms with the
@@ -384,6 +387,61 @@ ATTN_API int attn_mla_decode_paged(const void* q, const void* cache, const int32
                                    int d_rope, int num_blocks, int block_size, int max_blocks_per_seq,
                                    int max_seq_len, float scale, void* workspace, size_t workspace_bytes,
                                    int32_t* status, attn_stream_t stream);
+
+/*
+ * attn_prefill_paged_varlen_workspace_bytes - bytes of device workspace
+ * attn_prefill_paged_varlen needs on the current device for head dimension d
+ * (about 39 MB at d = 128): the partial outputs of work cut between two
+ * multiprocessors, whose number does not depend on the batch. 0 for a bad d.
+ */
+ATTN_API size_t attn_prefill_paged_varlen_workspace_bytes(int d);
+
+/*
+ * attn_prefill_paged_varlen - the newest n_b = cu_q[b + 1] - cu_q[b] positions
+ * of every sequence attend to its seq_lens[b] cached tokens through the block
+ * table ("Module 09", "Chunked Prefill" and continuous batching: chunks of
+ * prompts and decoding sequences in one batch). Query row i of sequence b sits
+ * at position seq_lens[b] - n_b + i; masks as in attn_prefill_paged, with the
+ * sink positions and learned sink logits of attn_decode_paged_window.
+ *
+ *   q            [T, Hq, d] bf16, rows of all sequences packed   read
+ *   k_cache,
+ *   v_cache      [num_blocks, block_size, Hkv, d] bf16           read
+ *   block_table  [B, max_blocks_per_seq] int32                   read: only entries of blocks
+ *                with a key that some row of the batch's work on them sees
+ *   cu_q         [B + 1] int32, row offsets, ascending           read
+ *   seq_lens     [B] int32, cached tokens, the new ones included read
+ *   sinks        [Hq] fp32 learned sink logits, or NULL          read
+ *   o            [T, Hq, d] bf16                                 written
+ *   lse          [T, Hq] fp32 (natural log, sink included), or NULL   written
+ *   n_sink       with a window: the first n_sink positions stay visible
+ *   workspace    caller-owned, 16-byte aligned; contents before and after do not matter;
+ *                one call at a time
+ * Rows of o and lse outside [cu_q[0], cu_q[B]) are left as they were, so a
+ * batch may be padded to a fixed T; a sequence may have no rows. Nothing may
+ * overlap o, lse or the workspace.
+ * V's values must be finite in every block a row sees a key of (a masked key's
+ * probability of 0 times infinity would not be 0); slots past seq_lens[b], and
+ * blocks no row sees, may hold anything.
+ *
+ * Device checks (ATTN_STATUS_BIT_DEVICE_CHECK): a sequence with rows and a
+ * length below their number or above max_seq_len, or with offsets out of order
+ * or past T, gets NaN rows (those inside the tensor); a table entry outside the
+ * pool gives NaN in the rows that need it.
+ *
+ * Errors (nothing is launched): ATTN_ERR_INVALID_ARG for NULL or misaligned
+ * pointers, bad sizes, Hq % Hkv != 0, a table row shorter than max_seq_len, a
+ * bad mask, window or scale, n_sink without a window or above max_seq_len;
+ * ATTN_ERR_UNSUPPORTED for d other than 64 or 128, block_size other than 16,
+ * 32, 64 or 128, T * Hq of 2^31 or more or max_seq_len above 2^30;
+ * ATTN_ERR_WORKSPACE; ATTN_ERR_CUDA when a launch fails.
+ */
+ATTN_API int attn_prefill_paged_varlen(const void* q, const void* k_cache, const void* v_cache,
+                                       const int32_t* block_table, const int32_t* cu_q, const int32_t* seq_lens,
+                                       const float* sinks, void* o, float* lse, int B, int T, int Hq, int Hkv, int d,
+                                       int num_blocks, int block_size, int max_blocks_per_seq, int max_seq_len,
+                                       int mask_kind, int window, int n_sink, float scale, void* workspace,
+                                       size_t workspace_bytes, int32_t* status, attn_stream_t stream);
 
 /*
  * attn_paged_extend - give every sequence the cache blocks its new tokens

@@ -112,3 +112,28 @@ def test_norm_rope_backward_rejects_bad_arguments(kw, code):
 def test_norm_rope_backward_workspace_rejects_bad_sizes():
     f = _lib.lib().attn_qk_norm_rope_backward_workspace_bytes
     assert f(0, 8, 4, 2, 128) == 0 and f(1, 8, 4, 2, 96) == 0
+
+
+def _varlen(**kw):
+    a = dict(q=FAKE, kc=FAKE, vc=FAKE, bt=FAKE, cu=FAKE, sl=FAKE, sinks=NULL, o=FAKE, lse=NULL, B=2, T=10, Hq=8, Hkv=2, d=128,
+             nb=10, bs=16, mb=8, msl=128, mask=1, window=0, n_sink=0, scale=0.1, ws=FAKE, wsb=1 << 30)
+    a.update(kw)
+    return _lib.lib().attn_prefill_paged_varlen(*a.values(), NULL, NULL)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=NULL), INVALID), (dict(vc=NULL), INVALID), (dict(bt=NULL), INVALID), (dict(cu=NULL), INVALID),
+    (dict(sl=NULL), INVALID), (dict(o=NULL), INVALID), (dict(q=ctypes.c_void_p(0x10008)), INVALID), (dict(cu=ODD), INVALID),
+    (dict(sinks=ODD), INVALID), (dict(lse=ODD), INVALID), (dict(B=0), INVALID), (dict(T=0), INVALID), (dict(nb=0), INVALID),
+    (dict(Hq=6, Hkv=4), INVALID), (dict(mb=7), INVALID), (dict(msl=0), INVALID), (dict(mask=7), INVALID),
+    (dict(mask=2, window=0), INVALID), (dict(n_sink=1), INVALID), (dict(mask=2, window=4, n_sink=-1), INVALID),
+    (dict(mask=2, window=4, n_sink=129), INVALID), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(d=96), UNSUPPORTED), (dict(bs=8, mb=16), UNSUPPORTED), (dict(bs=48, mb=3), UNSUPPORTED),
+    (dict(T=1 << 28), UNSUPPORTED), (dict(mb=1 << 27, msl=(1 << 30) + 1), UNSUPPORTED),
+])
+def test_varlen_rejects_bad_arguments(kw, code):
+    assert _varlen(**kw) == code
+
+
+def test_varlen_workspace_rejects_bad_head_dimensions():
+    assert _lib.lib().attn_prefill_paged_varlen_workspace_bytes(96) == 0

@@ -55,16 +55,22 @@ constexpr int kVlThreads = 384;
 constexpr int kVlWarps = kVlThreads / 32;
 constexpr int kVlTmaWarp = 8;
 constexpr int kVlMmaWarp = 9;
+constexpr int kVlPlanWarp = 10;
+constexpr int kVlTmaVWarp = 11;
 constexpr int kVlRows = 2 * kBM;  // rows of an item
 // the register split of the prefill kernel: 256 x 224 + 128 x 56 = 384 x 168
 constexpr uint32_t kVlRegsSoftmax = 224;
 constexpr uint32_t kVlRegsControl = 56;
 static_assert(256 * kVlRegsSoftmax + 128 * kVlRegsControl == kVlThreads * 168, "register split");
 constexpr float kVlRescale = 8.0f;  // base 2: the maximum moves only past this (p <= 2^8)
-// What a key tile costs on the line, and what an item costs besides.
-constexpr int kCostWide = 3, kCostNarrow = 2, kCostItem = 3;
-// A CTA's stretch is at least this long: shorter cuts cost more in joining than they save.
-constexpr int kMinStretch = 4 * kCostWide;
+// What a key costs on the line, and what an item costs besides, in proportion to
+// the cycles measured: a wide tile of 128 keys 3,650 (d = 128) and 3,300 (d = 64),
+// a narrow one COSTN, an item's ends 5,000.
+constexpr int kCostWide = 20, kCostItem = 28 * kBN;
+template <int D>
+constexpr int kCostNarrow = D == 128 ? 11 : 8;
+// A CTA's stretch holds a tile at least (a piece of every item it passes through).
+constexpr int kMinStretch = kCostWide * kBN;
 
 template <int D>
 struct VlCfg {
@@ -72,31 +78,37 @@ struct VlCfg {
   static constexpr int kHalves = D / 64;
   static constexpr int kTile = kHalves * kHalf;
   static constexpr int kStages = (D == 128) ? 2 : 4;  // K ring and V ring, each
+  // A narrow item's V ring has one slot more, in the place of the second Q tile:
+  // a V tile waits for its softmax, 1 us after its K tile was used.
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kQOff + 2 * kTile;
   static constexpr int kVOff = kKOff + kStages * kTile;
   static constexpr int kStageOff = kVOff + kStages * kTile;  // 4 KB per softmax warp
   static constexpr int kBarOff = kStageOff + 8 * 4096;
-  static constexpr int kBytes = kBarOff + 256;
+  static constexpr int kBytes = kBarOff + 384;
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 bytes
-  static_assert(kAlloc <= 232448 - 512, "shared memory per CTA (512 bytes are static)");
+  static_assert(kAlloc <= 232448 - 1024, "shared memory per CTA (under 1 KB is static)");
   __host__ __device__ static constexpr uint32_t col_s(int x) { return x ? 128u : 0u; }
   __host__ __device__ static constexpr uint32_t col_o(int x) { return 256u + static_cast<uint32_t>(x * D); }
 };
 
 enum : int {
   kVbQFull = 0,
-  kVbKFull = 1,
-  kVbVFull = 5,
-  kVbKEmpty = 9,
-  kVbVEmpty = 13,
-  kVbSFull = 17,
-  kVbPLo = 19,
-  kVbPHi = 21,
-  kVbOFinal = 23,
-  kVbDrain = 25,
-  kVbQEmpty = 26,
+  kVbKFull = 1,    // + stage (up to 4)
+  kVbVFull = 5,    // + slot (up to 5)
+  kVbKEmpty = 10,  // + stage
+  kVbVEmpty = 14,  // + slot
+  kVbSFull = 19,   // + team
+  kVbPLo = 21,     // + team: probabilities of keys 0-63 written
+  kVbPHi = 23,     // + team: probabilities of keys 64-127 written
+  kVbOFinal = 25,  // + team
+  kVbDrain = 27,
+  kVbQEmpty = 28,
+  kVbPiece = 29,      // + entry of the piece ring (4)
+  kVbPieceDone = 33,  // + entry
 };
+constexpr int kVbTmemSlot = 312, kVbAbort = 316;  // bytes behind the barriers
+constexpr int kPieces = 4;                        // pieces worked out ahead
 
 // An item whose first piece is CTA c's last: what the joining grid needs of it.
 struct VarlenSplit {
@@ -116,6 +128,8 @@ struct VarlenParams {
   float2* part_ml;     // [2 G][256]
   VarlenSplit* splits;  // [G]
   int B, T, Hq, group, gsz, hchunks, tpt, units;  // gsz heads a tile, hchunks tiles a group, units = Hkv * hchunks
+  int tph;             // tokens of 64 rows
+  int tma_out;         // a warp's 32 rows are whole tokens: they leave as one box
   int row_magic;       // ceil(2^16 / gsz): row * magic >> 16 = row / gsz for rows below 128
   int mask_kind, window, n_sink, max_blocks, block_size, num_blocks, max_seq_len;
   float scale_log2;
@@ -136,13 +150,12 @@ __device__ __forceinline__ VlSeq seq_at(const VarlenParams& p, int b) {
 
 // One stretch of rows of a sequence: its tokens, the keys some row sees (the
 // sink positions [0, sink_end) and [key_lo, key_end)), and the T key tiles that
-// hold them: tile j of the list is key tile j, or j + skip behind the sinks'.
+// hold them: nst tiles from position 0, the others from `base` on, the block
+// with key_lo (a tile may start at any block).
 struct VlGeom {
-  int tok0, ntok, pos_lo, key_lo, key_end, sink_end, nst, skip, T;
+  int tok0, ntok, pos_lo, key_lo, key_end, sink_end, nst, base, T;
   bool wide;
-  __device__ __forceinline__ int key_tile(int j) const { return j < nst ? j : j + skip; }
-  __device__ __forceinline__ int tile_cost() const { return wide ? kCostWide : kCostNarrow; }
-  __device__ __forceinline__ int cost() const { return kCostItem + T * tile_cost(); }
+  __device__ __forceinline__ int tile_key(int j) const { return j < nst ? j * kBN : base + (j - nst) * kBN; }
 };
 __device__ __forceinline__ VlGeom geom_at(const VarlenParams& p, int n, int nk, int rt) {
   VlGeom g;
@@ -154,31 +167,40 @@ __device__ __forceinline__ VlGeom geom_at(const VarlenParams& p, int n, int nk, 
   g.key_lo = p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? max(0, g.pos_lo - p.window + 1) : 0;
   g.sink_end = min(p.n_sink, g.key_lo);
   g.nst = (g.sink_end + kBN - 1) / kBN;
-  const int lo = max(g.key_lo / kBN, g.nst);
-  g.skip = lo - g.nst;
-  g.T = g.nst + max(0, (g.key_end - 1) / kBN - lo + 1);
+  g.base = max(g.key_lo & ~(p.block_size - 1), g.nst * kBN);
+  g.T = g.nst + max(0, (g.key_end - g.base + kBN - 1) / kBN);
   return g;
 }
 __device__ __forceinline__ int row_tiles(const VarlenParams& p, int n) { return (n + 2 * p.tpt - 1) / (2 * p.tpt); }
 
-// The cost of one unit (all row tiles for one K/V head) of this lane's
-// sequence; warp-collective, since a long chunk's tiles are summed by all lanes.
-__device__ __forceinline__ long long unit_cost(const VarlenParams& p, const VlSeq& s) {
-  constexpr int kAlone = 8;
-  const int lane = threadIdx.x & 31;
-  const int nrt = row_tiles(p, s.n);
-  long long c = 0;
-  if (nrt <= kAlone)
-    for (int rt = 0; rt < nrt; ++rt) c += geom_at(p, s.n, s.nk, rt).cost();
-  for (unsigned big = __ballot_sync(0xffffffffu, nrt > kAlone); big != 0; big &= big - 1) {
-    const int src = __ffs(big) - 1;
-    const int n = __shfl_sync(0xffffffffu, s.n, src), nk = __shfl_sync(0xffffffffu, s.nk, src);
-    long long part = 0;
-    for (int rt = lane; rt < row_tiles(p, n); rt += 32) part += geom_at(p, n, nk, rt).cost();
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xffffffffu, part, d);
-    if (lane == src) c = part;
+// Length on the line of the first R row tiles of a sequence of one K/V head, in
+// closed form: kCostItem an item, and its keys (with a window at most so many:
+// whole blocks and tiles of sinks; every key tile must start inside its item's
+// length). All R tiles are wide but a sequence's last.
+template <int D>
+__device__ __forceinline__ long long line_of(const VarlenParams& p, int n, int nk, int R) {
+  const int nrt = row_tiles(p, n), S = 2 * p.tpt;
+  const long long pos0 = nk - n;
+  const bool last = R == nrt;  // the last one may be shorter, and narrow
+  const long long F = last ? R - 1 : R;
+  const int tail = n - (nrt - 1) * S;
+  long long keys, tail_keys;
+  if (p.mask_kind == ATTN_MASK_FULL) {
+    keys = F * nk;
+    tail_keys = nk;
+  } else if (p.mask_kind == ATTN_MASK_CAUSAL) {
+    keys = F * pos0 + S * (F * (F + 1) / 2);
+    tail_keys = nk;
+  } else {
+    const int W = p.window, extra = ((p.n_sink + kBN - 1) / kBN) * kBN + kBN;
+    // the first F0 row tiles start at a position that sees position 0
+    const int reach = W - 1 - static_cast<int>(pos0);
+    const long long F0 = reach < 0 ? 0 : min(static_cast<long long>(reach / S + 1), F);
+    keys = F0 * pos0 + S * (F0 * (F0 + 1) / 2) + (F - F0) * (S + W - 1) + F * extra;
+    tail_keys = min(nk, tail + W - 1) + extra;
   }
+  long long c = R * static_cast<long long>(kCostItem) + keys * kCostWide;
+  if (last) c += tail_keys * (tail > p.tpt ? kCostWide : kCostNarrow<D>);
   return c;
 }
 
@@ -190,32 +212,58 @@ struct VlPlan {
   long long s;       // where that item starts
 };
 
-// Every role walks the CTA's stretch with its own copy of this.
+// A place in the CTA's stretch.
 struct VlWalk {
   int b, u, rt, nrt;
   long long s;
   VlSeq sq;
 };
-// A piece of an item: key tiles [j0, j1) of its list.
+// A piece of an item: key tiles [j0, j0 + nt) of its list, nt = 0 behind the last piece.
 struct VlPiece {
   VlGeom g;
-  int j0, j1, b, nk, row0, u;
-  long long x0;  // where the item's first tile stands on the line
+  int j0, nt, b, nk, row0, kvh, head0, nheads;
+  bool half;   // a narrow item of at most 64 rows: team 1 has them in its lanes 64 and up
+  bool whole;
+  int slot;    // of its partial output
+  int pieces;  // of the item, when this is the first of several
 };
-// The next piece of the stretch that has any key tile; false at its end.
-__device__ __forceinline__ bool next_piece(const VarlenParams& p, const VlPlan& pl, VlWalk& w, VlPiece& out) {
+// The first tile that starts at or after `x` (keys' cost from the item's first tile).
+template <int D>
+__device__ __forceinline__ int tile_from(long long x, const VlGeom& g) {
+  constexpr unsigned long long kWide = kCostWide * kBN, kNarrow = kCostNarrow<D> * kBN;
+  if (x <= 0) return 0;
+  const unsigned long long v = x, t = g.wide ? (v + kWide - 1) / kWide : (v + kNarrow - 1) / kNarrow;
+  return t < static_cast<unsigned long long>(g.T) ? static_cast<int>(t) : g.T;
+}
+// The next piece of the stretch that has any key tile; nt = 0 at its end.
+template <int D>
+__device__ __forceinline__ void next_piece(const VarlenParams& p, const VlPlan& pl, int cta, VlWalk& w, VlPiece& out) {
   while (w.s < pl.end) {
-    out.g = geom_at(p, w.sq.n, w.sq.nk, w.rt);
-    out.row0 = w.sq.row0 + out.g.tok0;
+    const VlGeom g = geom_at(p, w.sq.n, w.sq.nk, w.rt);
+    const long long x0 = w.s + kCostItem;  // where the item's first tile stands
+    const int j0 = tile_from<D>(pl.start - x0, g), j1 = tile_from<D>(pl.end - x0, g);
+    const int kvh = w.u / p.hchunks, hc = w.u - kvh * p.hchunks;
+    out.g = g;
+    out.j0 = j0;
+    out.nt = j1 - j0;
+    out.half = g.ntok <= p.tph;
     out.b = w.b;
     out.nk = w.sq.nk;
-    out.u = w.u;
-    out.x0 = w.s + kCostItem;
-    const int c = out.g.tile_cost();
-    const long long a = pl.start - out.x0, e = pl.end - out.x0;
-    out.j0 = a <= 0 ? 0 : static_cast<int>(min((a + c - 1) / c, static_cast<long long>(out.g.T)));
-    out.j1 = e <= 0 ? 0 : static_cast<int>(min((e + c - 1) / c, static_cast<long long>(out.g.T)));
-    w.s += out.g.cost();
+    out.row0 = w.sq.row0 + g.tok0;
+    out.kvh = kvh;
+    out.head0 = kvh * p.group + hc * p.gsz;
+    out.nheads = min(p.gsz, p.group - hc * p.gsz);
+    out.whole = j0 == 0 && j1 == g.T;
+    out.slot = cta * 2 + (j0 == 0 ? 1 : 0);
+    out.pieces = 0;
+    if (j0 == 0 && j1 < g.T) {
+      // up to the CTA that holds the item's last tile, by the line's arithmetic
+      const long long last = x0 + static_cast<long long>(g.T - 1) * (g.wide ? kCostWide : kCostNarrow<D>) * kBN;
+      out.pieces = static_cast<int>(((last + 1) * pl.G - 1) / pl.total) - cta + 1;
+    }
+    int keys = g.key_end - g.key_lo;
+    if (p.mask_kind == ATTN_MASK_SLIDING_WINDOW) keys += ((p.n_sink + kBN - 1) / kBN) * kBN + kBN;
+    w.s = x0 + static_cast<long long>(keys) * (g.wide ? kCostWide : kCostNarrow<D>);
     if (++w.rt == w.nrt) {
       w.rt = 0;
       if (++w.u == p.units) {
@@ -227,10 +275,30 @@ __device__ __forceinline__ bool next_piece(const VarlenParams& p, const VlPlan& 
         }
       }
     }
-    if (out.j0 < out.j1) return true;
+    if (j0 < j1) return;
   }
-  return false;
+  out.nt = 0;
 }
+__device__ __forceinline__ VarlenSplit split_of(const VlPiece& pc) {
+  return VarlenSplit{pc.pieces, pc.row0, pc.g.ntok, pc.head0, pc.nheads, pc.g.wide ? 1 : 0, 0, 0};
+}
+// The V ring: slots are taken in turn, a wide item's without the last one. Both
+// ends step through it alike; bit s is the parity of slot s's next use.
+template <int STAGES>
+struct VRing {
+  int next = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void enter(bool wide) {
+    if (wide && next == STAGES) next = 0;
+  }
+  __device__ __forceinline__ uint32_t phase(int s) const { return (parity >> s) & 1u; }
+  __device__ __forceinline__ int take(bool wide) {
+    const int s = next;
+    parity ^= 1u << s;
+    next = s + 1 < STAGES + (wide ? 0 : 1) ? s + 1 : 0;
+    return s;
+  }
+};
 
 // Every (row, key) pair of a tile is visible: rows at positions [qa, qb], keys [k0, k0 + 128).
 __device__ __forceinline__ bool vl_tile_is_full(const VarlenParams& p, int qa, int qb, int k0, int nk) {
@@ -240,18 +308,114 @@ __device__ __forceinline__ bool vl_tile_is_full(const VarlenParams& p, int qa, i
   return full;
 }
 
+// One key tile of a team's rows: scores from TMEM (colS), the mask, the running
+// maximum and sum of this thread's row, the output row (colO) rescaled where the
+// maximum moved, and the probabilities back over the scores, in two halves.
+// EDGE: visible are the columns [cmin, cmax] and those before csink.
+template <int D, bool EDGE>
+__device__ __forceinline__ void softmax_tile(const VarlenParams& p, uint32_t colS, uint32_t colO, uint32_t bar_lo,
+                                             uint32_t bar_hi, int cmin, int cmax, int csink, bool row_valid,
+                                             float& m_used, float& l_sum) {
+  const float sl2 = p.scale_log2;
+  // On a tile at the mask's edge: the visible keys of this row, a word for
+  // each 32 columns, and whether the warp's rows see none or all of them. What
+  // none sees is not computed; the select stands only where some see and some not.
+  uint32_t vis[kBN / 32], none = 0, some = 0;
+  if (EDGE) {
+#pragma unroll
+    for (int cc = 0; cc < kBN / 32; ++cc) {
+      const int lo = cmin - 32 * cc, hi = cmax - 32 * cc, sk = csink - 32 * cc;
+      const uint32_t from = lo <= 0 ? ~0u : (lo > 31 ? 0u : ~0u << lo);
+      const uint32_t to = hi < 0 ? 0u : (hi > 30 ? ~0u : (2u << hi) - 1u);
+      const uint32_t sink = sk <= 0 ? 0u : (sk > 31 ? ~0u : (1u << sk) - 1u);
+      vis[cc] = row_valid ? (from | sink) & to : 0u;
+      if (!__any_sync(0xffffffffu, vis[cc] != 0u)) none |= 1u << cc;
+      if (!__all_sync(0xffffffffu, vis[cc] == ~0u || !row_valid)) some |= 1u << cc;
+    }
+  }
+  uint32_t raw[kBN];
+#pragma unroll
+  for (int cc = 0; cc < kBN / 32; ++cc)
+    tmem_ld_32x32b_x32(colS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[cc * 32]));
+  tc_wait_ld();
+  float sv[kBN];
+#pragma unroll
+  for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(raw[c]);
+  float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+  for (int cc = 0; cc < kBN / 32; ++cc) {
+    if (EDGE && (none >> cc & 1u)) continue;
+    if (EDGE && (some >> cc & 1u)) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) sv[cc * 32 + e] = vis[cc] >> e & 1u ? sv[cc * 32 + e] : -INFINITY;
+    }
+#pragma unroll
+    for (int c = cc * 32; c < cc * 32 + 32; c += 8) {
+      mx0 = max3f(mx0, sv[c], sv[c + 1]);
+      mx1 = max3f(mx1, sv[c + 2], sv[c + 3]);
+      mx2 = max3f(mx2, sv[c + 4], sv[c + 5]);
+      mx3 = max3f(mx3, sv[c + 6], sv[c + 7]);
+    }
+  }
+  const float m_new = fmaxf(m_used, max3f(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
+  bool rescale_o = false;
+  float factor = 1.f;
+  if (m_new > m_used + kVlRescale) {  // also true for the first visible key (m_used = -inf)
+    const bool prev_finite = (m_used != -INFINITY);
+    factor = prev_finite ? fast_exp2(m_used - m_new) : 0.f;
+    l_sum *= factor;
+    rescale_o = prev_finite;
+    m_used = m_new;
+  }
+  // The score barrier was committed after this team's previous P V: O is stable.
+  if (__any_sync(0xffffffffu, rescale_o)) rescale_row_t<D>(colO, rescale_o ? factor : 1.f);
+  // a row with nothing visible yet uses m = 0
+  const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
+  float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
+#pragma unroll
+  for (int cc = 0; cc < kBN / 32; ++cc) {
+    uint32_t pk[16];
+    if (EDGE && (none >> cc & 1u)) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = 0u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int c = cc * 32 + 2 * e;
+        const float2 xv =
+            ffma2(make_float2(sv[c], sv[c + 1]), make_float2(sl2, sl2), make_float2(neg_m, neg_m));
+        float2 pv;
+        pv.x = fast_exp2(xv.x);
+        pv.y = fast_exp2(xv.y);
+        float2& acc = (e & 3) == 0 ? acc0 : (e & 3) == 1 ? acc1 : (e & 3) == 2 ? acc2 : acc3;
+        acc = fadd2(acc, pv);
+        pk[e] = pack_bf16x2(pv.x, pv.y);
+      }
+    }
+    tmem_st_32x32b_x16(colS + cc * 16, pk);  // over score columns already consumed
+    if (cc == 1 || cc == 3) {
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(cc == 1 ? bar_lo : bar_hi);
+    }
+  }
+  l_sum += ((acc0.x + acc0.y) + (acc1.x + acc1.y)) + ((acc2.x + acc2.y) + (acc3.x + acc3.y));
+}
+
 __device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
 
 template <int D>
 __global__ void __launch_bounds__(kVlThreads, 1)
-    prefill_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vr,
+    prefill_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qh,
+                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ CUtensorMap tm_vr, const __grid_constant__ CUtensorMap tm_o,
                           const VarlenParams p) {
   using C = VlCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long sums_s[kVlWarps];
   __shared__ VlPlan plan_s;
-  __shared__ volatile int bad_s[4];  // a table entry outside the pool, by item (mod 4)
+  __shared__ VlPiece pieces_s[kPieces];
+  __shared__ volatile int bad_s[kPieces];  // the piece's blocks have an entry outside the pool
   const uint32_t raw_u32 = smem_u32(smem_raw);
   const uint32_t sbase = (raw_u32 + 1023u) & ~1023u;  // swizzled tiles need 1024-byte alignment
   uint8_t* smem = smem_raw + (sbase - raw_u32);
@@ -263,16 +427,18 @@ __global__ void __launch_bounds__(kVlThreads, 1)
 
   const uint32_t bars = sbase + C::kBarOff;
   auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + 224);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + 228);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kBarOff + kVbTmemSlot);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kBarOff + kVbAbort);
 
   if (threadIdx.x == 0) {
     mbar_init(bar(kVbQFull), 1);
     mbar_init(bar(kVbQEmpty), 1);
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(kVbKFull + s), 1);
-      mbar_init(bar(kVbVFull + s), 1);
       mbar_init(bar(kVbKEmpty + s), 1);
+    }
+    for (int s = 0; s < 5; ++s) {
+      mbar_init(bar(kVbVFull + s), 1);
       mbar_init(bar(kVbVEmpty + s), 1);
     }
     for (int x = 0; x < 2; ++x) {
@@ -281,10 +447,13 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       mbar_init(bar(kVbPHi + x), kBM);
       mbar_init(bar(kVbOFinal + x), 1);
     }
+    for (int s = 0; s < kPieces; ++s) {
+      mbar_init(bar(kVbPiece + s), 1);
+      mbar_init(bar(kVbPieceDone + s), 11);  // both TMA warps, the MMA thread, 8 softmax warps
+    }
     mbar_init(bar(kVbDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
-    p.splits[cta].pieces = 0;
   }
   if (warp == kVlMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -300,7 +469,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
     for (int r = 0; r < rounds; ++r) {
       const int b = r * kVlThreads + static_cast<int>(threadIdx.x);
       sq = b < p.B ? seq_at(p, b) : VlSeq{0, 0, 0, false};
-      uc = unit_cost(p, sq);
+      uc = sq.n > 0 ? line_of<D>(p, sq.n, sq.nk, row_tiles(p, sq.n)) : 0;
       sum += uc * p.units;
     }
 #pragma unroll
@@ -317,7 +486,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       const int b = r * kVlThreads + static_cast<int>(threadIdx.x);
       if (rounds > 1) {
         sq = b < p.B ? seq_at(p, b) : VlSeq{0, 0, 0, false};
-        uc = unit_cost(p, sq);
+        uc = sq.n > 0 ? line_of<D>(p, sq.n, sq.nk, row_tiles(p, sq.n)) : 0;
       }
       const long long c = uc * p.units;
       long long inc = c;
@@ -339,13 +508,13 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         long long off = start - mine;
         const int u = static_cast<int>(off / uc);
         off -= u * uc;
-        long long at = 0;
-        int rt = 0;
-        for (;; ++rt) {
-          const int ic = geom_at(p, sq.n, sq.nk, rt).cost();
-          if (off < at + ic) break;
-          at += ic;
+        int rt = 0;  // the last row tile that starts at or before it
+        for (int hi = row_tiles(p, sq.n); hi - rt > 1;) {
+          const int mid = (rt + hi) >> 1;
+          if (line_of<D>(p, sq.n, sq.nk, mid) <= off) rt = mid;
+          else hi = mid;
         }
+        const long long at = rt > 0 ? line_of<D>(p, sq.n, sq.nk, rt) : 0;
         plan_s.b = b;
         plan_s.u = u;
         plan_s.rt = rt;
@@ -379,131 +548,158 @@ __global__ void __launch_bounds__(kVlThreads, 1)
     }
     return w;
   };
+  // piece `it`, worked out ahead by the plan warp; the reader gives the entry back
+  auto piece_wait = [&](int it) -> bool {
+    return mbar_wait_bounded(bar(kVbPiece + it % kPieces), (it / kPieces) & 1, budget, abort_flag);
+  };
+  auto piece_done = [&](int it) { mbar_arrive(bar(kVbPieceDone + it % kPieces)); };
 
   if (warp >= kVlTmaWarp) {
     regs_dec<kVlRegsControl>();
-    if (warp == kVlTmaWarp) {
-      // ---------------------------------------------------------- TMA producer
+    if (warp == kVlTmaWarp || warp == kVlTmaVWarp) {
+      // ---------------------------------------------------------- TMA producers: Q and K by one warp, V by the other
+      // (a box of a block of 16 tokens takes about as long to issue as to move:
+      // one warp for both kept HBM at 73 % where two reach REACH %).
       // Lane 0 waits on the ring and arms the barriers, lane e copies block e of a
-      // key tile. A block that no row of the item sees, that lies past the sequence
-      // or whose entry is outside the pool is asked for at block num_blocks, which
-      // TMA fills with zeros: nothing is read of it, its keys are masked, and its
-      // probabilities of 0 meet zeros in V. In the block where the sequence ends, V
-      // goes row by row (all lanes), zeros behind the end, for the same reason: 0
-      // times what a pool holds there could be NaN. K's rows there are masked.
+      // key tile, its table entry read one tile ahead. A block that no row of the
+      // item sees, that lies past the sequence or whose entry is outside the pool is
+      // asked for at block num_blocks, which TMA fills with zeros: nothing is read of
+      // it, its keys are masked, and its probabilities of 0 meet zeros in V. In the
+      // block where the sequence ends, V goes row by row (all lanes), zeros behind
+      // the end, for the same reason: 0 times what a pool holds there could be NaN.
+      // K's rows there are masked.
+      const bool k_warp = warp == kVlTmaWarp;
       if (lane == 0) {
-        prefetch_tmap(&tm_q);
-        prefetch_tmap(&tm_k);
-        prefetch_tmap(&tm_v);
+        prefetch_tmap(k_warp ? &tm_k : &tm_v);
+        if (k_warp) prefetch_tmap(&tm_q);
       }
       const int bs = p.block_size, boxes = kBN / bs;
-      VlWalk w = first_walk();
-      VlPiece pc;
-      int g = 0, k_issued = 0, v_issued = 0, it = 0;
+      int g = 0, it = 0;  // K tiles and items so far
+      VRing<C::kStages> vr;
       bool ok = true;
-      while (ok && next_piece(p, pl, w, pc)) {
+      for (;; ++it) {
+        ok = __all_sync(0xffffffffu, piece_wait(it));
+        if (!ok) break;
+        const int flag = it % kPieces;
+        const VlPiece pc = pieces_s[flag];
         const VlGeom& gm = pc.g;
-        const int nt = pc.j1 - pc.j0;
-        const int kvh = pc.u / p.hchunks, hc = pc.u - kvh * p.hchunks;
-        const int flag = it & 3;
-        if (lane == 0) bad_s[flag] = 0;
+        const int nt = pc.nt;
+        if (nt == 0) break;
+        if (k_warp && lane == 0) bad_s[flag] = 0;
         __syncwarp();
         auto fetch = [&](int j) -> int {
-          const int key = gm.key_tile(pc.j0 + j) * kBN + lane * bs;
+          const int key = gm.tile_key(pc.j0 + j) + lane * bs;
           const bool seen = lane < boxes && key < gm.key_end && (key + bs > gm.key_lo || key < gm.sink_end);
           int ent = p.num_blocks;
           if (seen) {
             ent = __ldg(p.block_table + static_cast<size_t>(pc.b) * p.max_blocks + key / bs);
             if (ent < 0 || ent >= p.num_blocks) {
               ent = p.num_blocks;
-              bad_s[flag] = 1;
+              if (k_warp) bad_s[flag] = 1;
             }
           }
           __syncwarp();
           return ent;
         };
-        auto load_k = [&](uint32_t dst, uint32_t full, int ent) {
-          if (lane < boxes)
-            for (int hh = 0; hh < C::kHalves; ++hh)
-              tma_load_4d(dst + lane * bs * 128 + hh * C::kHalf, &tm_k, full, hh * 64, kvh, 0, ent);
-        };
-        auto load_v = [&](uint32_t dst, uint32_t full, int j, int ent) {
-          const int key = gm.key_tile(pc.j0 + j) * kBN + lane * bs;
-          const bool part = lane < boxes && key < pc.nk && key + bs > pc.nk && ent != p.num_blocks;
-          if (lane < boxes && !part)
-            for (int hh = 0; hh < C::kHalves; ++hh)
-              tma_load_4d(dst + lane * bs * 128 + hh * C::kHalf, &tm_v, full, hh * 64, kvh, 0, ent);
-          const unsigned who = __ballot_sync(0xffffffffu, part);
-          if (who != 0) {
-            const int src = __ffs(who) - 1;
-            const int phys = __shfl_sync(0xffffffffu, ent, src);
-            const int valid = pc.nk - __shfl_sync(0xffffffffu, key, src);  // 1 .. bs - 1 rows hold tokens
-            for (int i = lane; i < bs * C::kHalves; i += 32) {
-              const int slot = i / C::kHalves, hh = i - slot * C::kHalves;
-              tma_load_4d(dst + (src * bs + slot) * 128 + hh * C::kHalf, &tm_vr, full, hh * 64, kvh, slot,
-                          slot < valid ? phys : p.num_blocks);
-            }
-          }
-        };
-        int ent_k = fetch(0), ent_v = p.num_blocks;
+        int ent = fetch(0);
+        // The second Q tile's place is a V slot of narrow items: the item before has
+        // read its Q, and a wide item's Q waits for the slot's last V tile.
         bool armed = true;
         if (lane == 0) {
           armed = (it == 0) || mbar_wait_bounded(bar(kVbQEmpty), (it - 1) & 1, budget, abort_flag);
-          if (armed) {
-            const int tiles = gm.wide ? 2 : 1;
-            mbar_arrive_expect_tx(bar(kVbQFull), tiles * C::kHalves * p.gsz * p.tpt * 128);
-            for (int x = 0; x < tiles; ++x)
-              for (int hh = 0; hh < C::kHalves; ++hh)
-                tma_load_3d(sbase + C::kQOff + x * C::kTile + hh * C::kHalf, &tm_q, bar(kVbQFull), hh * 64,
-                            kvh * p.group + hc * p.gsz, pc.row0 + x * p.tpt);
+          if (k_warp) {
+            if (armed && gm.wide)
+              armed = mbar_wait_bounded(bar(kVbVEmpty + C::kStages), vr.phase(C::kStages) ^ 1u, budget, abort_flag);
+            if (armed) {
+              // two boxes: both tiles of a wide item, or the same 64 rows twice
+              const int boxes_q = gm.wide || pc.half ? 2 : 1, tokens = pc.half ? p.tph : p.tpt;
+              mbar_arrive_expect_tx(bar(kVbQFull), boxes_q * C::kHalves * p.gsz * tokens * 128);
+              for (int x = 0; x < boxes_q; ++x)
+                for (int hh = 0; hh < C::kHalves; ++hh)
+                  tma_load_3d(sbase + C::kQOff + x * (pc.half ? 64 * 128 : C::kTile) + hh * C::kHalf,
+                              pc.half ? &tm_qh : &tm_q, bar(kVbQFull), hh * 64, pc.head0,
+                              pc.row0 + (pc.half ? 0 : x * p.tpt));
+            }
           }
         }
         ok = __shfl_sync(0xffffffffu, armed, 0);
         if (!ok) break;
-        ++it;
-        for (int i = 0; i <= nt; ++i) {
-          if (i < nt) {
+        vr.enter(gm.wide);
+        for (int i = 0; i < nt; ++i) {
+          const int next = i + 1 < nt ? fetch(i + 1) : p.num_blocks;
+          if (k_warp) {
             const int gi = g + i, s = gi % C::kStages, rnd = gi / C::kStages;
             if (lane == 0) {
               armed = (rnd == 0) || mbar_wait_bounded(bar(kVbKEmpty + s), (rnd - 1) & 1, budget, abort_flag);
               if (armed) mbar_arrive_expect_tx(bar(kVbKFull + s), C::kTile);
             }
             ok = __shfl_sync(0xffffffffu, armed, 0);
-            if (!ok) break;
-            load_k(sbase + C::kKOff + s * C::kTile, bar(kVbKFull + s), ent_k);
-            k_issued = gi + 1;
-          }
-          if (i >= 1) {
-            const int gv = g + i - 1, s = gv % C::kStages, rnd = gv / C::kStages;
+            if (!ok) {
+              g += i;
+              break;
+            }
+            vr.take(gm.wide);
+            const uint32_t dst = sbase + C::kKOff + s * C::kTile + lane * bs * 128;
+            if (lane < boxes)
+              for (int hh = 0; hh < C::kHalves; ++hh)
+                tma_load_4d(dst + hh * C::kHalf, &tm_k, bar(kVbKFull + s), hh * 64, pc.kvh, 0, ent);
+          } else {
+            const int s = vr.next;
             if (lane == 0) {
-              armed = (rnd == 0) || mbar_wait_bounded(bar(kVbVEmpty + s), (rnd - 1) & 1, budget, abort_flag);
+              armed = mbar_wait_bounded(bar(kVbVEmpty + s), vr.phase(s) ^ 1u, budget, abort_flag);
               if (armed) mbar_arrive_expect_tx(bar(kVbVFull + s), C::kTile);
             }
             ok = __shfl_sync(0xffffffffu, armed, 0);
             if (!ok) break;
-            load_v(sbase + C::kVOff + s * C::kTile, bar(kVbVFull + s), i - 1, ent_v);
-            v_issued = gv + 1;
+            vr.take(gm.wide);
+            const uint32_t dst = sbase + (s < C::kStages ? C::kVOff + s * C::kTile : C::kQOff + C::kTile);
+            const uint32_t full = bar(kVbVFull + s);
+            const int key = gm.tile_key(pc.j0 + i) + lane * bs;
+            const bool part = lane < boxes && key < pc.nk && key + bs > pc.nk && ent != p.num_blocks;
+            if (lane < boxes && !part)
+              for (int hh = 0; hh < C::kHalves; ++hh)
+                tma_load_4d(dst + lane * bs * 128 + hh * C::kHalf, &tm_v, full, hh * 64, pc.kvh, 0, ent);
+            const unsigned who = __ballot_sync(0xffffffffu, part);
+            if (who != 0) {
+              const int src = __ffs(who) - 1;
+              const int phys = __shfl_sync(0xffffffffu, ent, src);
+              const int valid = pc.nk - __shfl_sync(0xffffffffu, key, src);  // 1 .. bs - 1 rows hold tokens
+              for (int r = lane; r < bs * C::kHalves; r += 32) {
+                const int slot = r / C::kHalves, hh = r - slot * C::kHalves;
+                tma_load_4d(dst + (src * bs + slot) * 128 + hh * C::kHalf, &tm_vr, full, hh * 64, pc.kvh, slot,
+                            slot < valid ? phys : p.num_blocks);
+              }
+            }
           }
-          ent_v = ent_k;
-          if (i + 1 < nt) ent_k = fetch(i + 1);
+          ent = next;
+        }
+        if (!ok) {
+          ++it;  // this item's Q is in flight
+          break;
         }
         g += nt;
+        __syncwarp();
+        if (lane == 0) piece_done(it);
       }
       if (lane == 0) {
         if (!ok) raise_abort(abort_flag, p.status);
-        // Drain: the newest copy of every stage and of Q has landed before the CTA may exit.
+        // Drain: this warp's newest copy of every stage has landed before the CTA may exit.
         volatile int never = 0;
-        if (it > 0) mbar_wait_bounded(bar(kVbQFull), (it - 1) & 1, kDrainBudgetCycles, &never);
-        for (int j = (k_issued > C::kStages ? k_issued - C::kStages : 0); j < k_issued; ++j)
-          mbar_wait_bounded(bar(kVbKFull + j % C::kStages), (j / C::kStages) & 1, kDrainBudgetCycles, &never);
-        for (int j = (v_issued > C::kStages ? v_issued - C::kStages : 0); j < v_issued; ++j)
-          mbar_wait_bounded(bar(kVbVFull + j % C::kStages), (j / C::kStages) & 1, kDrainBudgetCycles, &never);
+        if (k_warp) {
+          if (it > 0) mbar_wait_bounded(bar(kVbQFull), (it - 1) & 1, kDrainBudgetCycles, &never);
+          for (int j = (g > C::kStages ? g - C::kStages : 0); j < g; ++j)
+            mbar_wait_bounded(bar(kVbKFull + j % C::kStages), (j / C::kStages) & 1, kDrainBudgetCycles, &never);
+        } else {
+          for (int s = 0; s <= C::kStages; ++s)
+            mbar_wait_bounded(bar(kVbVFull + s), vr.phase(s) ^ 1u, kDrainBudgetCycles, &never);
+        }
       }
     } else if (warp == kVlMmaWarp && lane == 0) {
       // ---------------------------------------------------------- MMA issuer
       const uint64_t dq0 = desc_sw128(sbase + C::kQOff, 16, 1024);
       const uint64_t dk0 = desc_sw128(sbase + C::kKOff, 16, 1024);
       const uint64_t dv0 = desc_sw128(sbase + C::kVOff, C::kHalf, 1024);
+      const uint64_t dvq = desc_sw128(sbase + C::kQOff + C::kTile, C::kHalf, 1024);  // the V ring's last slot
       constexpr uint64_t kTileUnits = C::kTile >> 4;
       auto wait_k = [&](int g) -> bool {
         const bool r = mbar_wait_bounded(bar(kVbKFull + g % C::kStages), (g / C::kStages) & 1, budget, abort_flag);
@@ -518,8 +714,8 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       };
       int cnt[2] = {0, 0};  // score tiles of each team so far
       // O_x (+)= P_x V, each half of P as it lands
-      auto pv = [&](int x, int g, bool first) -> bool {
-        const uint64_t dv = dv0 + static_cast<uint64_t>(g % C::kStages) * kTileUnits;
+      auto pv = [&](int x, int s, bool first) -> bool {
+        const uint64_t dv = s < C::kStages ? dv0 + static_cast<uint64_t>(s) * kTileUnits : dvq;
         if (!mbar_wait_bounded(bar(kVbPLo + x), cnt[x] & 1, budget, abort_flag)) return false;
         tc_fence_after();
         mma_pv<D, 0, 4>(tmem + C::col_o(x), tmem + C::col_s(x), dv, first);
@@ -529,13 +725,19 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         ++cnt[x];
         return true;
       };
-      VlWalk w = first_walk();
-      VlPiece pc;
       int g = 0, it = 0;
+      VRing<C::kStages> vr;
       bool ok = true;
-      while (ok && next_piece(p, pl, w, pc)) {
-        const int nt = pc.j1 - pc.j0;
-        const bool wide = pc.g.wide;
+      for (; ok; ++it) {
+        if (!piece_wait(it)) {
+          ok = false;
+          break;
+        }
+        const int nt = pieces_s[it % kPieces].nt;
+        const bool wide = pieces_s[it % kPieces].g.wide;
+        piece_done(it);
+        if (nt == 0) break;
+        vr.enter(wide);
         const int teams = wide ? 2 : 1, ahead = wide ? 1 : 2;  // key tiles a score runs ahead of its P V
         if (!mbar_wait_bounded(bar(kVbQFull), it & 1, budget, abort_flag)) {
           ok = false;
@@ -557,8 +759,10 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           if (j == nt - 1) tc_commit(bar(kVbQEmpty));
         }
         for (int j = 0; j < nt && ok; ++j) {
-          const int gj = g + j, s = gj % C::kStages, jn = j + ahead;
-          if (!mbar_wait_bounded(bar(kVbVFull + s), (gj / C::kStages) & 1, budget, abort_flag)) {
+          const int jn = j + ahead;
+          const uint32_t parity = vr.phase(vr.next);
+          const int s = vr.take(wide);
+          if (!mbar_wait_bounded(bar(kVbVFull + s), parity, budget, abort_flag)) {
             ok = false;
             break;
           }
@@ -566,7 +770,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
             const int x = wide ? t : (j & 1);
             // P V of key tile j, then (in issue order, so they overwrite P only after it is
             // read) this team's next scores
-            if (!pv(x, gj, wide ? j == 0 : j < 2)) {
+            if (!pv(x, s, wide ? j == 0 : j < 2)) {
               ok = false;
               break;
             }
@@ -586,27 +790,42 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           }
         }
         g += nt;
-        ++it;
       }
       if (!ok) raise_abort(abort_flag, p.status);
       // Drain: every MMA this thread issued has completed before TMEM is freed.
       tc_commit(bar(kVbDrain));
       volatile int never = 0;
       mbar_wait_bounded(bar(kVbDrain), 0, kDrainBudgetCycles, &never);
-    } else if (warp > kVlMmaWarp) {
-      // ---------------------------------------------------------- rows of sequences that have no valid lengths
+    } else if (warp == kVlPlanWarp) {
+      // ---------------------------------------------------------- the pieces of the stretch, a few ahead of their use
+      if (lane == 0) {
+        VlWalk w = first_walk();
+        p.splits[cta].pieces = 0;
+        for (int it = 0;; ++it) {
+          const int e = it % kPieces;
+          if (it >= kPieces && !mbar_wait_bounded(bar(kVbPieceDone + e), (it / kPieces - 1) & 1, budget, abort_flag))
+            break;
+          VlPiece pc;
+          next_piece<D>(p, pl, cta, w, pc);
+          pieces_s[e] = pc;
+          if (pc.nt > 0 && pc.pieces > 0) p.splits[cta] = split_of(pc);
+          mbar_arrive(bar(kVbPiece + e));
+          if (pc.nt == 0) break;
+        }
+      }
+      __syncwarp();
+      // then the rows of sequences whose lengths do not fit
       for (int b = cta; b < p.B; b += gridDim.x) {
         const VlSeq sq = seq_at(p, b);
         if (!sq.bad) continue;
-        const int t = threadIdx.x - 32 * (kVlMmaWarp + 1);
-        if (t == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
+        if (lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
         const int r0 = max(0, sq.row0), r1 = min(p.T, __ldg(p.cu_q + b + 1));
         for (int r = r0; r < r1; ++r) {
           __nv_bfloat16* row = p.o + static_cast<size_t>(r) * p.Hq * D;
-          for (int i = t; i < p.Hq * D / 8; i += 64)
+          for (int i = lane; i < p.Hq * D / 8; i += 32)
             reinterpret_cast<uint4*>(row)[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
           if (p.lse != nullptr)
-            for (int i = t; i < p.Hq; i += 64) p.lse[static_cast<size_t>(r) * p.Hq + i] = NAN;
+            for (int i = lane; i < p.Hq; i += 32) p.lse[static_cast<size_t>(r) * p.Hq + i] = NAN;
         }
       }
     }
@@ -618,23 +837,30 @@ __global__ void __launch_bounds__(kVlThreads, 1)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t colS = lane_base + C::col_s(x);
     const uint32_t colO = lane_base + C::col_o(x);
-    const float sl2 = p.scale_log2;
-    const int rtok = (r * p.row_magic) >> 16, rhead = r - rtok * p.gsz;  // this row's token and head in a tile
-    VlWalk w = first_walk();
-    VlPiece pc;
     int cnt = 0, fin = 0, it = 0;  // this team's score tiles, finished outputs; items
     bool ok = true;
-    for (; next_piece(p, pl, w, pc); ++it) {
+    for (; ok; ++it) {
+      ok = __all_sync(0xffffffffu, piece_wait(it));
+      if (!ok) break;
+      const VlPiece& pc = pieces_s[it % kPieces];
       const VlGeom& gm = pc.g;
-      const int nt = pc.j1 - pc.j0;
+      const int nt = pc.nt;
+      if (nt == 0) break;
       const bool wide = gm.wide;
-      const int kvh = pc.u / p.hchunks, hc = pc.u - kvh * p.hchunks;
-      const int head0 = kvh * p.group + hc * p.gsz, nheads = min(p.gsz, p.group - hc * p.gsz);
+      const int nheads = pc.nheads, head0 = pc.head0;
       const int t0 = wide ? x * p.tpt : 0;                 // the tile's first token in the item
       const int ntok = min(gm.ntok - t0, p.tpt);           // and its tokens (a wide item's second tile has some)
-      const int qa = gm.pos_lo + t0, qpos = qa + rtok;
-      const bool row_valid = rtok < ntok && rhead < nheads;
-      const bool active = (warp & 3) * 32 < ntok * p.gsz;  // the warp has rows of the item
+      const int qa = gm.pos_lo + t0;
+      // This thread's row of the item's tile, its token and head. A narrow item of at
+      // most 64 rows stands in the lanes 64 and up for team 1: its warps then run on
+      // the SM partitions that team 0's leave idle (warps 0 and 4 share one, and at
+      // 128 exponentials a row it was the limit: SAMEPART cycles a tile at d = 64).
+      const int shift = pc.half && x == 1 ? 2 : 0;  // in warps
+      const int wr = (warp & 3) - shift, row = wr * 32 + lane;
+      const int rtok = (row * p.row_magic) >> 16, rhead = row - rtok * p.gsz;
+      const bool active = wr >= 0 && wr * 32 < ntok * p.gsz;  // the warp has rows of the item
+      const bool row_valid = active && rtok < ntok && rhead < nheads;
+      const float sink2 = p.sinks != nullptr && row_valid ? __ldg(p.sinks + head0 + rhead) * kLog2e : -INFINITY;
       float m_used = -INFINITY;  // max the exponentials are taken against (base 2)
       float l_sum = 0.f;         // running sum of 2^(s - m_used)
       for (int j = wide ? 0 : x; j < nt && ok; j += wide ? 1 : 2, ++cnt) {
@@ -645,70 +871,16 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           mbar_arrive(bar(kVbPHi + x));
           continue;
         }
-        const int k0 = gm.key_tile(pc.j0 + j) * kBN;
+        const int k0 = gm.tile_key(pc.j0 + j);
         tc_fence_after();
-        uint32_t raw[kBN];
-#pragma unroll
-        for (int c = 0; c < kBN / 32; ++c)
-          tmem_ld_32x32b_x32(colS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[c * 32]));
-        tc_wait_ld();
-        float sv[kBN];
-#pragma unroll
-        for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(raw[c]);
-        if (!vl_tile_is_full(p, qa, qa + ntok - 1, k0, pc.nk)) {
-          // visible keys of this row: columns [cmin, cmax], and those before csink
-          const int cmax = (p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : qpos) - k0;
-          const int cmin = p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? qpos - k0 - p.window + 1 : 0;
-          const int csink = p.n_sink - k0;
-#pragma unroll
-          for (int c = 0; c < kBN; ++c) sv[c] = ((c >= cmin || c < csink) && c <= cmax) ? sv[c] : -INFINITY;
-        }
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kBN; c += 8) {
-          mx0 = max3f(mx0, sv[c], sv[c + 1]);
-          mx1 = max3f(mx1, sv[c + 2], sv[c + 3]);
-          mx2 = max3f(mx2, sv[c + 4], sv[c + 5]);
-          mx3 = max3f(mx3, sv[c + 6], sv[c + 7]);
-        }
-        const float m_new = fmaxf(m_used, max3f(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
-        bool rescale_o = false;
-        float factor = 1.f;
-        if (m_new > m_used + kVlRescale) {  // also true for the first visible key (m_used = -inf)
-          const bool prev_finite = (m_used != -INFINITY);
-          factor = prev_finite ? fast_exp2(m_used - m_new) : 0.f;
-          l_sum *= factor;
-          rescale_o = prev_finite;
-          m_used = m_new;
-        }
-        // The score barrier was committed after this team's previous P V: O is stable.
-        if (__any_sync(0xffffffffu, rescale_o)) rescale_row_t<D>(colO, rescale_o ? factor : 1.f);
-        // a row with nothing visible yet uses m = 0
-        const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
-#pragma unroll
-        for (int cc = 0; cc < kBN / 32; ++cc) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int c = cc * 32 + 2 * e;
-            const float2 xv =
-                ffma2(make_float2(sv[c], sv[c + 1]), make_float2(sl2, sl2), make_float2(neg_m, neg_m));
-            float2 pv;
-            pv.x = fast_exp2(xv.x);
-            pv.y = fast_exp2(xv.y);
-            float2& acc = (e & 3) == 0 ? acc0 : (e & 3) == 1 ? acc1 : (e & 3) == 2 ? acc2 : acc3;
-            acc = fadd2(acc, pv);
-            pk[e] = pack_bf16x2(pv.x, pv.y);
-          }
-          tmem_st_32x32b_x16(colS + cc * 16, pk);  // over score columns already consumed
-          if (cc == 1 || cc == 3) {
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(bar((cc == 1 ? kVbPLo : kVbPHi) + x));
-          }
-        }
-        l_sum += ((acc0.x + acc0.y) + (acc1.x + acc1.y)) + ((acc2.x + acc2.y) + (acc3.x + acc3.y));
+        // A tile inside the mask runs without any of the edge's branches.
+        if (vl_tile_is_full(p, qa, qa + ntok - 1, k0, pc.nk))
+          softmax_tile<D, false>(p, colS, colO, bar(kVbPLo + x), bar(kVbPHi + x), 0, 0, 0, true, m_used, l_sum);
+        else
+          softmax_tile<D, true>(p, colS, colO, bar(kVbPLo + x), bar(kVbPHi + x),
+                                p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? qa + rtok - k0 - p.window + 1 : 0,
+                                (p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : qa + rtok) - k0, p.n_sink - k0, row_valid, m_used,
+                                l_sum);
       }
       const bool took_part = wide || nt > x;
       if (ok && took_part)
@@ -718,23 +890,30 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       tc_fence_after();
       if (!active || !took_part) {
         tc_fence_before();
+        __syncwarp();
+        if (lane == 0) piece_done(it);
         continue;
       }
+
+      // After an expired wait the accumulators are read all the same and come out as NaN.
+      const uint32_t stage = sbase + C::kStageOff + warp * 4096;
+      if (lane == 0) bulk_wait_read_all();  // the last output has left the staging box
+      __syncwarp();
 
       // ---- the two teams of a narrow item are joined: both know both sums, team 1
       // hands its output over in 32-column pieces through its staging box
       const bool join = !wide && nt > 1;
-      const uint32_t stage = sbase + C::kStageOff + warp * 4096;
+      const int other_warp = x == 0 ? warp + 4 + (pc.half ? 2 : 0) : wr;
       float f = 1.f;
       if (join) {
         float2* mine = reinterpret_cast<float2*>(smem + C::kStageOff + warp * 4096);
-        mine[lane] = make_float2(m_used, l_sum);
-        pair_barrier(1 + (warp & 3));
-        const float2 other = reinterpret_cast<float2*>(smem + C::kStageOff + (warp ^ 4) * 4096)[lane];
-        pair_barrier(1 + (warp & 3));  // read before the boxes are written again
+        mine[lane] = make_float2(m_used, ok ? l_sum : NAN);
+        pair_barrier(1 + wr);
+        const float2 other = reinterpret_cast<float2*>(smem + C::kStageOff + other_warp * 4096)[lane];
+        pair_barrier(1 + wr);  // read before the boxes are written again
         const float m = fmaxf(m_used, other.x);
         f = m_used == -INFINITY ? 0.f : exp2f(m_used - m);
-        l_sum = l_sum * f + (other.x == -INFINITY ? 0.f : other.y * exp2f(other.x - m));
+        l_sum = l_sum * f + (other.x == -INFINITY ? 0.f * other.y : other.y * exp2f(other.x - m));
         m_used = m;
       }
       if (join && x == 1) {
@@ -742,71 +921,66 @@ __global__ void __launch_bounds__(kVlThreads, 1)
 #pragma unroll
         for (int c32 = 0; c32 < D / 32; ++c32) {
           uint32_t ov[32];
-          if (ok) {
-            tmem_ld_32x32b_x32(colO + c32 * 32, ov);
-            tc_wait_ld();
+          tmem_ld_32x32b_x32(colO + c32 * 32, ov);
+          tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) box[e * 32 + lane] = f == 0.f ? 0.f : __uint_as_float(ov[e]) * f;
-          }
-          pair_barrier(1 + (warp & 3));
-          pair_barrier(1 + (warp & 3));
+          for (int e = 0; e < 32; ++e) box[e * 32 + lane] = f == 0.f ? 0.f : __uint_as_float(ov[e]) * f;
+          pair_barrier(1 + wr);
+          pair_barrier(1 + wr);
         }
         tc_fence_before();
+        __syncwarp();
+        if (lane == 0) piece_done(it);
         continue;
       }
 
-      const bool whole = pc.j0 == 0 && pc.j1 == gm.T;
-      const bool out_ok = ok && bad_s[it & 3] == 0;
-      if (!out_ok && ok && lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
-      const int slot = cta * 2 + (pc.j0 == 0 ? 1 : 0);
-      float norm = 1.f;
+      const bool whole = pc.whole;
+      const bool bad = bad_s[it % kPieces] != 0;
+      if (bad && lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
+      float l = bad || !ok ? NAN : l_sum, norm = 1.f;
       if (whole) {
-        float m = m_used, l = l_sum, ff = 1.f;
-        if (p.sinks != nullptr && row_valid) {  // one more column with no value
-          const float sk = __ldg(p.sinks + head0 + rhead) * kLog2e;
-          m = fmaxf(m_used, sk);
+        float m = m_used, ff = 1.f;
+        if (p.sinks != nullptr) {  // one more column with no value
+          m = fmaxf(m_used, sink2);
           ff = exp2f(m_used - m);
-          l = l * ff + exp2f(sk - m);
+          l = l * ff + exp2f(sink2 - m);
         }
-        norm = out_ok ? ff / l : NAN;
+        norm = ff / l;
         if (row_valid && p.lse != nullptr)
-          p.lse[static_cast<size_t>(pc.row0 + t0 + rtok) * p.Hq + head0 + rhead] = out_ok ? (m + log2f(l)) * kLn2 : NAN;
+          p.lse[static_cast<size_t>(pc.row0 + t0 + rtok) * p.Hq + head0 + rhead] = (m + log2f(l)) * kLn2;
       } else {
-        p.part_ml[static_cast<size_t>(slot) * kVlRows + x * kBM + r] = make_float2(m_used, out_ok ? l_sum : NAN);
-        if (pc.j0 == 0 && threadIdx.x == 0) {
-          // the CTA that holds the item's last tile, by the line's arithmetic
-          const long long last = pc.x0 + static_cast<long long>(gm.T - 1) * gm.tile_cost();
-          const int c1 = static_cast<int>(((last + 1) * pl.G - 1) / pl.total);
-          p.splits[cta] = VarlenSplit{c1 - cta + 1, pc.row0, gm.ntok, head0, nheads, wide ? 1 : 0, 0, 0};
-        }
+        p.part_ml[static_cast<size_t>(pc.slot) * kVlRows + x * kBM + r] = make_float2(m_used, l);
       }
-      const float* box = reinterpret_cast<const float*>(smem + C::kStageOff + (warp + 4) * 4096);
+      const float* box = reinterpret_cast<const float*>(smem + C::kStageOff + other_warp * 4096);
+      // a warp's rows are whole tokens of the sequence: they leave as a box
+      const int wtok = p.tma_out ? 32 / p.gsz : 0;
+      const bool as_box = p.tma_out && (wr + 1) * wtok <= ntok;
 #pragma unroll
       for (int hh = 0; hh < D / 64; ++hh) {
+        if (hh > 0 && whole && as_box) {
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+        }
 #pragma unroll
         for (int q32 = 0; q32 < 2; ++q32) {
           uint32_t ov[32];
-          if (ok) {
-            tmem_ld_32x32b_x32(colO + hh * 64 + q32 * 32, ov);
-            tc_wait_ld();
-          }
+          tmem_ld_32x32b_x32(colO + hh * 64 + q32 * 32, ov);
+          tc_wait_ld();
           if (join) {
-            pair_barrier(1 + (warp & 3));
+            pair_barrier(1 + wr);
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               ov[e] = __float_as_uint((f == 0.f ? 0.f : __uint_as_float(ov[e]) * f) + box[e * 32 + lane]);
-            pair_barrier(1 + (warp & 3));
+            pair_barrier(1 + wr);
           }
           if (whole) {
 #pragma unroll
             for (int c4 = 0; c4 < 4; ++c4) {
               uint32_t w4[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float a0 = ok ? __uint_as_float(ov[c4 * 8 + 2 * e]) * norm : NAN;
-                const float a1 = ok ? __uint_as_float(ov[c4 * 8 + 2 * e + 1]) * norm : NAN;
-                w4[e] = pack_bf16x2(a0, a1);
-              }
+              for (int e = 0; e < 4; ++e)
+                w4[e] = pack_bf16x2(__uint_as_float(ov[c4 * 8 + 2 * e]) * norm,
+                                    __uint_as_float(ov[c4 * 8 + 2 * e + 1]) * norm);
               const uint32_t dst = stage + lane * 128 + (((q32 * 4 + c4) ^ (lane & 7)) << 4);
               asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst), "r"(w4[0]), "r"(w4[1]), "r"(w4[2]),
                            "r"(w4[3])
@@ -814,26 +988,30 @@ __global__ void __launch_bounds__(kVlThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int c4 = 0; c4 < 8; ++c4) {
-              const float4 v = ok ? make_float4(__uint_as_float(ov[4 * c4]), __uint_as_float(ov[4 * c4 + 1]),
-                                                __uint_as_float(ov[4 * c4 + 2]), __uint_as_float(ov[4 * c4 + 3]))
-                                  : make_float4(NAN, NAN, NAN, NAN);
-              p.part_o[(static_cast<size_t>(slot) * (D / 4) + hh * 16 + q32 * 8 + c4) * kVlRows + x * kBM + r] = v;
-            }
+            for (int c4 = 0; c4 < 8; ++c4)
+              p.part_o[(static_cast<size_t>(pc.slot) * (D / 4) + hh * 16 + q32 * 8 + c4) * kVlRows + x * kBM + r] =
+                  make_float4(__uint_as_float(ov[4 * c4]), __uint_as_float(ov[4 * c4 + 1]),
+                              __uint_as_float(ov[4 * c4 + 2]), __uint_as_float(ov[4 * c4 + 3]));
           }
         }
-        if (whole) {  // 8 lanes a row, 16 bytes each; only rows of this sequence and these heads
+        if (whole && as_box) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_o, stage, hh * 64, head0, pc.row0 + t0 + wr * wtok);
+            bulk_commit();
+          }
+        } else if (whole) {  // 8 lanes a row, 16 bytes each; only rows of this sequence and these heads
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int wr = i * 4 + (lane >> 3), c = lane & 7;
-            const int row = (warp & 3) * 32 + wr;
-            const int tk = (row * p.row_magic) >> 16, hd = row - tk * p.gsz;
+            const int sr = i * 4 + (lane >> 3), c = lane & 7;
+            const int tk = ((wr * 32 + sr) * p.row_magic) >> 16, hd = wr * 32 + sr - tk * p.gsz;
             if (tk < ntok && hd < nheads) {
               uint4 v;
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
                            : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                           : "r"(stage + wr * 128 + ((c ^ (wr & 7)) << 4)));
+                           : "r"(stage + sr * 128 + ((c ^ (sr & 7)) << 4)));
               __nv_bfloat16* dst =
                   p.o + (static_cast<size_t>(pc.row0 + t0 + tk) * p.Hq + head0 + hd) * D + hh * 64;
               reinterpret_cast<uint4*>(dst)[c] = v;
@@ -845,6 +1023,31 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       // The next item's first P V overwrites O: its P is announced only after
       // these loads completed (tcgen05.wait::ld above, fence before the arrive).
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) piece_done(it);
+    }
+    if (lane == 0) bulk_wait_all();  // output stores complete before the CTA exits
+    if (!ok) {
+      // a wait expired: every row of the pieces not reached becomes NaN
+      raise_abort(abort_flag, p.status);
+      VlWalk w = first_walk();
+      VlPiece pc;
+      for (int i = 0;; ++i) {
+        next_piece<D>(p, pl, cta, w, pc);
+        if (pc.nt == 0) break;
+        if (i < it) continue;
+        if (pc.pieces > 0 && threadIdx.x == 0) p.splits[cta] = split_of(pc);
+        const int rtok = (r * p.row_magic) >> 16, rhead = r - rtok * p.gsz, tok = x * p.tpt + rtok;
+        if (rtok >= p.tpt || tok >= pc.g.ntok || rhead >= pc.nheads) continue;
+        if (!pc.whole) {
+          p.part_ml[static_cast<size_t>(pc.slot) * kVlRows + x * kBM + r] = make_float2(0.f, NAN);
+          continue;
+        }
+        const size_t row = static_cast<size_t>(pc.row0 + tok) * p.Hq + pc.head0 + rhead;
+        for (int i8 = 0; i8 < D / 8; ++i8)
+          reinterpret_cast<uint4*>(p.o + row * D)[i8] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        if (p.lse != nullptr) p.lse[row] = NAN;
+      }
     }
   }
 
@@ -902,8 +1105,8 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_varlen_join_kernel(const
   }
 }
 
-// Packed queries [T, Hq, d] as a rank-3 tensor; box = 64 columns x heads x tokens.
-bool encode_packed_q(CUtensorMap* map, const void* base, int d, int hq, int tokens, int box_heads, int box_tokens) {
+// Packed rows [T, Hq, d] as a rank-3 tensor; box = 64 columns x heads x tokens.
+bool encode_packed(CUtensorMap* map, const void* base, int d, int hq, int tokens, int box_heads, int box_tokens) {
   const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encode_fn());
   if (enc == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(hq),
@@ -941,6 +1144,8 @@ int launch_varlen_t(const VarlenArgs& a, cudaStream_t stream) {
   p.hchunks = (p.group + p.gsz - 1) / p.gsz;
   p.tpt = kBM / p.gsz;
   p.units = a.Hkv * p.hchunks;
+  p.tph = 64 / p.gsz;
+  p.tma_out = 32 % p.gsz == 0;
   p.row_magic = (65536 + p.gsz - 1) / p.gsz;
   p.mask_kind = a.mask_kind;
   p.window = a.window;
@@ -951,8 +1156,11 @@ int launch_varlen_t(const VarlenArgs& a, cudaStream_t stream) {
   p.max_seq_len = a.max_seq_len;
   p.scale_log2 = a.scale * kLog2e;
   p.budget = wait_budget_cycles();
-  CUtensorMap tq, tk, tv, tvr;
-  if (!encode_packed_q(&tq, a.q, D, a.Hq, a.T, p.gsz, p.tpt) ||
+  CUtensorMap tq, tqh, tk, tv, tvr, to;
+  // maps that no piece uses (no 64-row form, no output box) stand for themselves
+  if (!encode_packed(&tq, a.q, D, a.Hq, a.T, p.gsz, p.tpt) ||
+      !encode_packed(&tqh, a.q, D, a.Hq, a.T, p.gsz, p.tph > 0 ? p.tph : 1) ||
+      !encode_packed(&to, a.o, D, a.Hq, a.T, p.gsz, p.tma_out ? 32 / p.gsz : 1) ||
       !encode_pool(&tk, a.k_cache, D, a.Hkv, a.block_size, a.num_blocks, a.block_size) ||
       !encode_pool(&tv, a.v_cache, D, a.Hkv, a.block_size, a.num_blocks, a.block_size) ||
       !encode_pool(&tvr, a.v_cache, D, a.Hkv, a.block_size, a.num_blocks, 1))
@@ -960,7 +1168,7 @@ int launch_varlen_t(const VarlenArgs& a, cudaStream_t stream) {
   constexpr int smem = VlCfg<D>::kAlloc;
   if (cudaFuncSetAttribute(prefill_varlen_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  prefill_varlen_kernel<D><<<a.sms, kVlThreads, smem, stream>>>(tq, tk, tv, tvr, p);
+  prefill_varlen_kernel<D><<<a.sms, kVlThreads, smem, stream>>>(tq, tqh, tk, tv, tvr, to, p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.sms, kJoinParts);

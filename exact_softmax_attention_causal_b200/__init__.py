@@ -385,7 +385,7 @@ def _entry(fn):
                 raise ValueError(f"stream is on {stream.device}, the inputs on {first.device}")
             with torch.cuda.stream(stream):
                 return fn(first, *args, **kw)
-        if first.device.index != torch.cuda.current_device():
+        if first.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(first.device):
                 return fn(first, *args, **kw)
         return fn(first, *args, **kw)
@@ -397,14 +397,15 @@ def _need_on(t, name: str, dtype, shape, dev, strided: bool = False) -> None:
     """One input or output: dtype, exact shape, device, and contiguous unless strided."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.get_device() == dev.index and t.shape == shape and (strided or t.is_contiguous()):
+        return  # most of a small call's time is the host's: the reasons are looked for only when there is one
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} must be a CUDA tensor on {dev}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not strided and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _need_dims(t, name: str, ndim: int, layout: str) -> None:
@@ -435,8 +436,9 @@ def _out_on(t, name: str, dtype, shape, dev):
     return t
 
 
-def _current() -> int:
-    return torch.cuda.current_stream().cuda_stream
+def _current(dev) -> int:
+    """The raw handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _addr(t) -> int:
@@ -496,12 +498,12 @@ def prefill_paged_varlen(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_s
                                               _addr(sinks), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, d, num_blocks,
                                               block_size, block_table.shape[1], int(max_seq_len), MASKS[mask],
                                               int(window), int(n_sink), float(scale), workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size(), _addr(status), _current())
+                                              workspace.numel() * workspace.element_size(), _addr(status), _current(dev))
     _lib.check(rc, "attn_prefill_paged_varlen")
     return out, lse
 
 
-def _table_args(seq_lens, second, second_name, block_table, free_blocks, num_free, seq_lens_out, num_free_out, status):
+def _table_args(seq_lens, second, second_name, block_table, free_blocks, num_free, status):
     _need_dims(seq_lens, "seq_lens", 1, "[B]")
     _need_dims(block_table, "block_table", 2, "[B, max_blocks]")
     _need_dims(free_blocks, "free_blocks", 1, "[capacity]")
@@ -512,7 +514,21 @@ def _table_args(seq_lens, second, second_name, block_table, free_blocks, num_fre
     _need_on(free_blocks, "free_blocks", i32, (free_blocks.shape[0],), dev)
     _need_on(num_free, "num_free", i32, (1,), dev)
     _need_status(status, dev)
-    return _out_on(seq_lens_out, "seq_lens_out", i32, (B,), dev), _out_on(num_free_out, "num_free_out", i32, (1,), dev)
+    return dev, B
+
+
+def _int32_outs(given, dev):
+    """Outputs [n] int32: those of (tensor or None, name, n) that the caller gave, the others out of one allocation."""
+    sizes = [n for t, _, n in given if t is None]
+    fresh = iter(torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes) if sizes else ())
+    outs = []
+    for t, name, n in given:
+        if t is None:
+            t = next(fresh)
+        else:
+            _need_on(t, name, torch.int32, (n,), dev)
+        outs.append(t)
+    return outs
 
 
 @_entry
@@ -531,17 +547,16 @@ def paged_extend(seq_lens, new_lens, block_table, free_blocks, num_free, block_s
     sequence that cannot be served gets the length -1 - seq_lens[b] (negative)
     and slots of -1, and sets the status bit. Keyword stream: the CUDA stream (default: the current one).
     """
-    seq_lens_out, num_free_out = _table_args(seq_lens, new_lens, "new_lens", block_table, free_blocks, num_free,
-                                             seq_lens_out, num_free_out, status)
-    dev, B, n = seq_lens.device, seq_lens.shape[0], max(0, int(max_tokens))
-    cu_q = _out_on(cu_q, "cu_q", torch.int32, (B + 1,), dev)
-    positions = _out_on(positions, "positions", torch.int32, (n,), dev)
-    slots = _out_on(slots, "slots", torch.int32, (n,), dev)
+    dev, B = _table_args(seq_lens, new_lens, "new_lens", block_table, free_blocks, num_free, status)
+    n = max(0, int(max_tokens))
+    seq_lens_out, num_free_out, cu_q, positions, slots = _int32_outs(
+        ((seq_lens_out, "seq_lens_out", B), (num_free_out, "num_free_out", 1), (cu_q, "cu_q", B + 1),
+         (positions, "positions", n), (slots, "slots", n)), dev)
     rc = _lib.lib().attn_paged_extend(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
                                       free_blocks.data_ptr(), num_free.data_ptr(), seq_lens_out.data_ptr(),
                                       num_free_out.data_ptr(), cu_q.data_ptr(), positions.data_ptr(),
                                       slots.data_ptr(), B, int(num_blocks), int(block_size), block_table.shape[1],
-                                      free_blocks.shape[0], int(max_tokens), _addr(status), _current())
+                                      free_blocks.shape[0], int(max_tokens), _addr(status), _current(dev))
     _lib.check(rc, "attn_paged_extend")
     return seq_lens_out, num_free_out, cu_q, positions, slots
 
@@ -552,12 +567,12 @@ def paged_release(seq_lens, finished, block_table, free_blocks, num_free, block_
     """Puts the blocks of the sequences with finished[b] != 0 (int32) back on
     the free list; returns (seq_lens_out, num_free_out), the finished lengths 0.
     A length -1 - L that paged_extend left counts as L. free_blocks is written from num_free on; in place as paged_extend."""
-    seq_lens_out, num_free_out = _table_args(seq_lens, finished, "finished", block_table, free_blocks, num_free,
-                                             seq_lens_out, num_free_out, status)
+    dev, B = _table_args(seq_lens, finished, "finished", block_table, free_blocks, num_free, status)
+    seq_lens_out, num_free_out = _int32_outs(((seq_lens_out, "seq_lens_out", B), (num_free_out, "num_free_out", 1)), dev)
     rc = _lib.lib().attn_paged_release(seq_lens.data_ptr(), finished.data_ptr(), block_table.data_ptr(),
                                        free_blocks.data_ptr(), num_free.data_ptr(), seq_lens_out.data_ptr(),
-                                       num_free_out.data_ptr(), seq_lens.shape[0], int(num_blocks), int(block_size),
-                                       block_table.shape[1], free_blocks.shape[0], _addr(status), _current())
+                                       num_free_out.data_ptr(), B, int(num_blocks), int(block_size),
+                                       block_table.shape[1], free_blocks.shape[0], _addr(status), _current(dev))
     _lib.check(rc, "attn_paged_release")
     return seq_lens_out, num_free_out
 
@@ -627,7 +642,7 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: flo
                                       _addr(q_weight), _addr(k_weight), w_bf16, cos.data_ptr(), sin.data_ptr(),
                                       _addr(positions), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, N,
                                       Hq, Hkv, d, rd, max_pos, float(eps), int(interleaved), _addr(status),
-                                      _current())
+                                      _current(dev))
     _lib.check(rc, "attn_qk_norm_rope")
     return q_out, k_out, v_out
 
@@ -663,7 +678,7 @@ def qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
                                             positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(),
                                             k_cache.data_ptr(), v_cache.data_ptr(), T, Hq, Hkv, d, num_blocks,
                                             block_size, rd, max_pos, float(eps), int(interleaved), _addr(status),
-                                            _current())
+                                            _current(dev))
     _lib.check(rc, "attn_qk_norm_rope_paged")
     return q_out
 
@@ -717,6 +732,6 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, pos
         w_bf16, cos.data_ptr(), sin.data_ptr(), _addr(positions), d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _STRIDES9(*dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]),
         _addr(dwq), _addr(dwk), B, N, Hq, Hkv, d, rd, max_pos, float(eps), int(interleaved), _addr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _addr(status), _current())
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _addr(status), _current(dev))
     _lib.check(rc, "attn_qk_norm_rope_backward")
     return dq, dk, dv, dwq, dwk

@@ -121,6 +121,8 @@ def _declare(lib):
 def lib() -> ctypes.CDLL:
     """The loaded library; raises RuntimeError when it is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

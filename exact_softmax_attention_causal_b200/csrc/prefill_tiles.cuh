@@ -65,6 +65,53 @@ __device__ __forceinline__ void mma_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_
   if constexpr (KK + 1 < END) mma_pv<D, KK + 1, END>(d_tmem, p_tmem, dv, first);
 }
 
+// Warp-collective forms: every lane of a converged warp executes them and the
+// lane that elect.sync picks issues four steps at a time. A branch on one lane
+// leaves the compiler to find the lane for every instruction: a step then took
+// about 100 cycles to issue, more than it takes to run at d = 64.
+// d (+)= A B over four steps of 16 along the head dimension, operands from their bases.
+template <uint32_t IDESC>
+__device__ __forceinline__ void mma_ss4_w(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, p, t;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " setp.ne.b32 p, %3, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %4, t;\n}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(accumulate), "n"(IDESC)
+      : "memory");
+}
+// The same with A in TMEM, 8 columns a step, and B 2 KB a step (16 keys of V).
+template <uint32_t IDESC>
+__device__ __forceinline__ void mma_ts4_w(uint32_t d_tmem, uint32_t a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred e, p, t;\n .reg .b32 a1, a2, a3;\n .reg .b64 b1, b2, b3;\n"
+      " setp.ne.b32 p, %3, 0;\n setp.eq.b32 t, 0, 0;\n"
+      " add.u32 a1, %1, 8;\n add.u32 a2, %1, 16;\n add.u32 a3, %1, 24;\n"
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
+      " elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %4, t;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, t;\n}\n" ::"r"(d_tmem),
+      "r"(a), "l"(b), "r"(accumulate), "n"(IDESC)
+      : "memory");
+}
+template <int D>
+__device__ __forceinline__ void mma_scores_w(uint32_t d_tmem, uint64_t dq, uint64_t dk) {
+  mma_ss4_w<idesc_bf16(kBM, kBN, 0)>(d_tmem, dq, dk, 0u);
+  if constexpr (D == 128) mma_ss4_w<idesc_bf16(kBM, kBN, 0)>(d_tmem, dq + 1024, dk + 1024, 1u);
+}
+// Half of one P V: keys 0-63 (half 0) or 64-127 of a tile.
+template <int D>
+__device__ __forceinline__ void mma_pv_w(uint32_t d_tmem, uint32_t p_tmem, uint64_t dv, int half, bool first) {
+  mma_ts4_w<idesc_bf16(kBM, D, 1)>(d_tmem, p_tmem + 32u * half, dv + 512ull * half, first && half == 0 ? 0u : 1u);
+}
+
 // Multiply this thread's TMEM output row by f (warp-collective).
 template <int D>
 __device__ __forceinline__ void rescale_row_t(uint32_t colO, float f) {

@@ -88,6 +88,10 @@ struct VlCfg {
   static constexpr int kBytes = kBarOff + 384;
   static constexpr int kAlloc = kBytes + 1024;  // slack to align the base to 1024 bytes
   static_assert(kAlloc <= 232448 - 1024, "shared memory per CTA (under 1 KB is static)");
+  // TMEM columns: scores of both teams (128 each; the probabilities overwrite the
+  // first 64), then outputs. (At d = 64 there is room for the probabilities beside
+  // the scores, so that a team's next scores need not wait for P V; measured, the
+  // wide tile stayed at 3,300 cycles and the narrow one at 1,900.)
   __host__ __device__ static constexpr uint32_t col_s(int x) { return x ? 128u : 0u; }
   __host__ __device__ static constexpr uint32_t col_o(int x) { return 256u + static_cast<uint32_t>(x * D); }
 };
@@ -694,106 +698,94 @@ __global__ void __launch_bounds__(kVlThreads, 1)
             mbar_wait_bounded(bar(kVbVFull + s), vr.phase(s) ^ 1u, kDrainBudgetCycles, &never);
         }
       }
-    } else if (warp == kVlMmaWarp && lane == 0) {
-      // ---------------------------------------------------------- MMA issuer
+    } else if (warp == kVlMmaWarp) {
+      // ---------------------------------------------------------- MMA issuer (the warp stays converged)
+      auto wait = [&](int i, uint32_t parity) -> bool {
+        const bool r = __all_sync(0xffffffffu, mbar_wait_bounded(bar(i), parity, budget, abort_flag));
+        tc_fence_after();
+        return r;
+      };
       const uint64_t dq0 = desc_sw128(sbase + C::kQOff, 16, 1024);
       const uint64_t dk0 = desc_sw128(sbase + C::kKOff, 16, 1024);
       const uint64_t dv0 = desc_sw128(sbase + C::kVOff, C::kHalf, 1024);
       const uint64_t dvq = desc_sw128(sbase + C::kQOff + C::kTile, C::kHalf, 1024);  // the V ring's last slot
       constexpr uint64_t kTileUnits = C::kTile >> 4;
       auto wait_k = [&](int g) -> bool {
-        const bool r = mbar_wait_bounded(bar(kVbKFull + g % C::kStages), (g / C::kStages) & 1, budget, abort_flag);
-        tc_fence_after();
-        return r;
+        return wait(kVbKFull + g % C::kStages, (g / C::kStages) & 1);
       };
       // team x's scores of key tile g (counted over the CTA's stretch) with Q tile qx
+      uint32_t p_par = 0;  // bit x: parity of team x's next probabilities
       auto issue_s = [&](int x, int qx, int g) {
-        mma_scores<D>(tmem + C::col_s(x), dq0 + static_cast<uint64_t>(qx) * kTileUnits,
+        mma_scores_w<D>(tmem + C::col_s(x), dq0 + static_cast<uint64_t>(qx) * kTileUnits,
                       dk0 + static_cast<uint64_t>(g % C::kStages) * kTileUnits);
-        tc_commit(bar(kVbSFull + x));
+        tc_commit_w(bar(kVbSFull + x));
       };
-      int cnt[2] = {0, 0};  // score tiles of each team so far
       // O_x (+)= P_x V, each half of P as it lands
       auto pv = [&](int x, int s, bool first) -> bool {
         const uint64_t dv = s < C::kStages ? dv0 + static_cast<uint64_t>(s) * kTileUnits : dvq;
-        if (!mbar_wait_bounded(bar(kVbPLo + x), cnt[x] & 1, budget, abort_flag)) return false;
-        tc_fence_after();
-        mma_pv<D, 0, 4>(tmem + C::col_o(x), tmem + C::col_s(x), dv, first);
-        if (!mbar_wait_bounded(bar(kVbPHi + x), cnt[x] & 1, budget, abort_flag)) return false;
-        tc_fence_after();
-        mma_pv<D, 4, 8>(tmem + C::col_o(x), tmem + C::col_s(x), dv, first);
-        ++cnt[x];
+        const uint32_t parity = (p_par >> x) & 1u;
+        if (!wait(kVbPLo + x, parity)) return false;
+        mma_pv_w<D>(tmem + C::col_o(x), tmem + C::col_s(x), dv, 0, first);
+        if (!wait(kVbPHi + x, parity)) return false;
+        mma_pv_w<D>(tmem + C::col_o(x), tmem + C::col_s(x), dv, 1, first);
+        p_par ^= 1u << x;
         return true;
       };
       int g = 0, it = 0;
       VRing<C::kStages> vr;
       bool ok = true;
       for (; ok; ++it) {
-        if (!piece_wait(it)) {
-          ok = false;
-          break;
-        }
+        ok = wait(kVbPiece + it % kPieces, (it / kPieces) & 1);
+        if (!ok) break;
         const int nt = pieces_s[it % kPieces].nt;
         const bool wide = pieces_s[it % kPieces].g.wide;
-        piece_done(it);
+        __syncwarp();
+        if (lane == 0) piece_done(it);
         if (nt == 0) break;
         vr.enter(wide);
         const int teams = wide ? 2 : 1, ahead = wide ? 1 : 2;  // key tiles a score runs ahead of its P V
-        if (!mbar_wait_bounded(bar(kVbQFull), it & 1, budget, abort_flag)) {
-          ok = false;
-          break;
-        }
+        ok = wait(kVbQFull, it & 1);
+        if (!ok) break;
         // the first scores of both teams
         for (int j = 0; j < min(ahead, nt) && ok; ++j) {
-          if (!wait_k(g + j)) {
-            ok = false;
-            break;
-          }
-          if (wide) {
-            issue_s(0, 0, g);
-            issue_s(1, 1, g);
-          } else {
-            issue_s(j, 0, g + j);
-          }
-          tc_commit(bar(kVbKEmpty + (g + j) % C::kStages));
-          if (j == nt - 1) tc_commit(bar(kVbQEmpty));
+          ok = wait_k(g + j);
+          if (!ok) break;
+          issue_s(wide ? 0 : j, 0, g + j);
+          if (wide) issue_s(1, 1, g);
+          tc_commit_w(bar(kVbKEmpty + (g + j) % C::kStages));
+          if (j == nt - 1) tc_commit_w(bar(kVbQEmpty));
         }
         for (int j = 0; j < nt && ok; ++j) {
           const int jn = j + ahead;
           const uint32_t parity = vr.phase(vr.next);
           const int s = vr.take(wide);
-          if (!mbar_wait_bounded(bar(kVbVFull + s), parity, budget, abort_flag)) {
-            ok = false;
-            break;
-          }
+          ok = wait(kVbVFull + s, parity);
           for (int t = 0; t < teams && ok; ++t) {
             const int x = wide ? t : (j & 1);
+            const bool last_team = t == teams - 1;
             // P V of key tile j, then (in issue order, so they overwrite P only after it is
             // read) this team's next scores
-            if (!pv(x, s, wide ? j == 0 : j < 2)) {
-              ok = false;
-              break;
-            }
-            if (jn >= nt) tc_commit(bar(kVbOFinal + x));
-            if (t == teams - 1) tc_commit(bar(kVbVEmpty + s));
+            ok = pv(x, s, wide ? j == 0 : j < 2);
+            if (!ok) break;
+            if (jn >= nt) tc_commit_w(bar(kVbOFinal + x));
+            if (last_team) tc_commit_w(bar(kVbVEmpty + s));
             if (jn < nt) {
-              if (t == 0 && !wait_k(g + jn)) {
-                ok = false;
-                break;
-              }
+              if (t == 0) ok = wait_k(g + jn);
+              if (!ok) break;
               issue_s(x, wide ? t : 0, g + jn);
-              if (t == teams - 1) {
-                tc_commit(bar(kVbKEmpty + (g + jn) % C::kStages));
-                if (jn == nt - 1) tc_commit(bar(kVbQEmpty));  // that was the item's last read of Q
+              if (last_team) {
+                tc_commit_w(bar(kVbKEmpty + (g + jn) % C::kStages));
+                if (jn == nt - 1) tc_commit_w(bar(kVbQEmpty));  // that was the item's last read of Q
               }
             }
           }
         }
         g += nt;
       }
-      if (!ok) raise_abort(abort_flag, p.status);
+      if (!ok && lane == 0) raise_abort(abort_flag, p.status);
+      __syncwarp();
       // Drain: every MMA this thread issued has completed before TMEM is freed.
-      tc_commit(bar(kVbDrain));
+      tc_commit_w(bar(kVbDrain));
       volatile int never = 0;
       mbar_wait_bounded(bar(kVbDrain), 0, kDrainBudgetCycles, &never);
     } else if (warp == kVlPlanWarp) {
@@ -879,8 +871,8 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         else
           softmax_tile<D, true>(p, colS, colO, bar(kVbPLo + x), bar(kVbPHi + x),
                                 p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? qa + rtok - k0 - p.window + 1 : 0,
-                                (p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : qa + rtok) - k0, p.n_sink - k0, row_valid, m_used,
-                                l_sum);
+                                (p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : qa + rtok) - k0, p.n_sink - k0, row_valid,
+                                m_used, l_sum);
       }
       const bool took_part = wide || nt > x;
       if (ok && took_part)

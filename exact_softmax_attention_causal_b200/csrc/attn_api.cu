@@ -441,8 +441,7 @@ size_t attn_qk_norm_rope_backward_workspace_bytes(int B, int N, int Hq, int Hkv,
   if (B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || (d != 64 && d != 128)) return 0;
   int sms = 0;
   if (current_sm_count(&sms) != ATTN_OK) return 0;
-  return static_cast<size_t>(norm_rope_bwd_ctas(static_cast<long long>(B) * N, Hq, Hkv, d, sms)) * 2 * d *
-         sizeof(float);
+  return norm_rope_bwd_workspace(norm_rope_bwd_strips(static_cast<long long>(B) * N, Hq, Hkv, d, sms), Hq, Hkv, d);
 }
 
 int attn_qk_norm_rope_backward(const void* q, const void* k, const int64_t* strides, const void* q_weight,
@@ -471,12 +470,13 @@ int attn_qk_norm_rope_backward(const void* q, const void* k, const int64_t* stri
   }
   int sms = 0;
   if (current_sm_count(&sms) != ATTN_OK) return ATTN_ERR_CUDA;
-  const int ctas = norm_rope_bwd_ctas(static_cast<long long>(B) * N, Hq, Hkv, d, sms);
-  if (norm && (!workspace || !aligned16(workspace) || workspace_bytes < static_cast<size_t>(ctas) * 2 * d * sizeof(float)))
+  const int strips = norm_rope_bwd_strips(static_cast<long long>(B) * N, Hq, Hkv, d, sms);
+  if (norm &&
+      (!workspace || !aligned16(workspace) || workspace_bytes < norm_rope_bwd_workspace(strips, Hq, Hkv, d)))
     return ATTN_ERR_WORKSPACE;
   const void* const dz[3] = {d_q, d_k, d_v};
   void* const dx[3] = {dq, dk, dv};
-  return launch_norm_rope_backward(a, dz, dx, sb, sn, sh, dq_weight, dk_weight, static_cast<float*>(workspace), ctas,
+  return launch_norm_rope_backward(a, dz, dx, sb, sn, sh, dq_weight, dk_weight, static_cast<float*>(workspace), strips,
                                    status, reinterpret_cast<cudaStream_t>(stream));
 }
 

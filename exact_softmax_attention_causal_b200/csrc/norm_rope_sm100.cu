@@ -16,9 +16,18 @@
 // backward reads x and dz), a few FMAs each. So a head row stays in registers
 // between its load and its store: d / 8 lanes hold 8 elements (16 bytes) each,
 // the mean is a shuffle reduction over them, and a rotation partner half a
-// rotated width away is rd / 16 lanes away, another shuffle. A group of lanes
-// takes kHeads head rows of one token: their loads are all in flight before
-// the first is used, and they share the token's angles.
+// rotated width away is rd / 16 lanes away: its raw 16 bytes come by 4 shuffles.
+// At a full HBM's pace an SM has 44 cycles for a warp's 512 bytes, so the
+// instructions count too: pairs of elements share one (f32x2), and weights and
+// angles are multiplied once a token, not once a head.
+//
+// A group of lanes takes up to kHeads heads of one tensor of one token, their
+// loads all in flight before the first is used. The groups of a CTA take the
+// same heads of consecutive tokens: a head's rows then lie together on the
+// [B, H, N, d] side (4 KB at d = 128), a token's heads on the other (1 KB).
+// With consecutive groups on the heads of one token instead, the 256-byte rows
+// went out N rows apart: 113 us for B = 4, N = 4096, 32 / 8 heads, against FWDUS us
+// now (FWDPC % of HBM); the backward pass 168 us against BWDUS us (BWDPC %).
 //
 // All arithmetic is in 32 bits; the result is rounded to bf16 once. The weight
 // gradients are summed in 32 bits in a fixed order: over a thread's rows, the
@@ -37,81 +46,82 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kHeads = 4;  // head rows a group has in flight
+constexpr int kBwdCtasPerSm = 4;
 
-struct Angles {
-  float c[8], s[8];  // per element; interleaved: s carries the sign too
-};
+using F2x4 = float2[4];  // a lane's 8 elements
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void unpack8(const uint4& v, F2x4& x) {
+  x[0] = unpack2(v.x), x[1] = unpack2(v.y), x[2] = unpack2(v.z), x[3] = unpack2(v.w);
 }
+__device__ __forceinline__ uint4 pack8(const F2x4& x) {
+  return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                    pack_bf16x2(x[3].x, x[3].y));
+}
+__device__ __forceinline__ float2 swap2(float2 v) { return make_float2(v.y, v.x); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// This lane's 8 weights, or nothing.
-__device__ __forceinline__ void load_weights(const void* w, int w_bf16, int lane, float (&out)[8]) {
+// This lane's 8 weights.
+__device__ __forceinline__ void load_weights(const void* w, int w_bf16, int lane, F2x4& out) {
   if (w_bf16) {
     unpack8(__ldg(reinterpret_cast<const uint4*>(w) + lane), out);
   } else {
     const float4 a = __ldg(reinterpret_cast<const float4*>(w) + 2 * lane);
     const float4 b = __ldg(reinterpret_cast<const float4*>(w) + 2 * lane + 1);
-    out[0] = a.x, out[1] = a.y, out[2] = a.z, out[3] = a.w;
-    out[4] = b.x, out[5] = b.y, out[6] = b.z, out[7] = b.w;
+    out[0] = make_float2(a.x, a.y), out[1] = make_float2(a.z, a.w);
+    out[2] = make_float2(b.x, b.y), out[3] = make_float2(b.z, b.w);
   }
 }
 
-// The angles of this lane's 8 elements at position m. Lanes from rd / 8 on hold
-// elements that pass through (cos 1, sin 0).
+// What the elements of a lane are multiplied with at position m: own element by
+// c, partner's by s (the sign of the rotation included; dir = -1 turns back).
+// Lanes from rd / 8 on hold elements that pass through: c = 1, s = 0, and a
+// partner of 0 (an infinity times 0 would be NaN).
 template <bool INTER>
 __device__ __forceinline__ void load_angles(const float* cos_t, const float* sin_t, long long m, int rd, int lane,
-                                            Angles& a) {
-  const int half_lanes = rd / 16;
+                                            float dir, F2x4& c, F2x4& s) {
   if (8 * lane >= rd) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) a.c[e] = 1.f, a.s[e] = 0.f;
+    for (int i = 0; i < 4; ++i) c[i] = both(1.f), s[i] = both(0.f);
     return;
   }
   if (INTER) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(cos_t + m * (rd / 2)) + lane);
-    const float4 s = __ldg(reinterpret_cast<const float4*>(sin_t + m * (rd / 2)) + lane);
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    const float4 cv = __ldg(reinterpret_cast<const float4*>(cos_t + m * (rd / 2)) + lane);
+    const float4 sv = __ldg(reinterpret_cast<const float4*>(sin_t + m * (rd / 2)) + lane);
+    const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a.c[2 * i] = a.c[2 * i + 1] = cc[i];
-      a.s[2 * i] = -ss[i];
-      a.s[2 * i + 1] = ss[i];
-    }
+    for (int i = 0; i < 4; ++i) c[i] = both(cc[i]), s[i] = make_float2(-dir * ss[i], dir * ss[i]);
   } else {
-    const bool upper = lane >= half_lanes;
-    const int f = 2 * (lane - (upper ? half_lanes : 0));
+    const bool upper = lane >= rd / 16;
+    const int f = 2 * (lane - (upper ? rd / 16 : 0));
     const float4* cp = reinterpret_cast<const float4*>(cos_t + m * (rd / 2)) + f;
     const float4* sp = reinterpret_cast<const float4*>(sin_t + m * (rd / 2)) + f;
     const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
-    const float sg = upper ? 1.f : -1.f;
-    a.c[0] = c0.x, a.c[1] = c0.y, a.c[2] = c0.z, a.c[3] = c0.w;
-    a.c[4] = c1.x, a.c[5] = c1.y, a.c[6] = c1.z, a.c[7] = c1.w;
-    a.s[0] = sg * s0.x, a.s[1] = sg * s0.y, a.s[2] = sg * s0.z, a.s[3] = sg * s0.w;
-    a.s[4] = sg * s1.x, a.s[5] = sg * s1.y, a.s[6] = sg * s1.z, a.s[7] = sg * s1.w;
+    const float sg = upper ? dir : -dir;
+    c[0] = make_float2(c0.x, c0.y), c[1] = make_float2(c0.z, c0.w);
+    c[2] = make_float2(c1.x, c1.y), c[3] = make_float2(c1.z, c1.w);
+    s[0] = make_float2(sg * s0.x, sg * s0.y), s[1] = make_float2(sg * s0.z, sg * s0.w);
+    s[2] = make_float2(sg * s1.x, sg * s1.y), s[3] = make_float2(sg * s1.z, sg * s1.w);
   }
 }
 
-// y turned by the angles (dir = 1) or back (dir = -1). `partner`: the warp lane
-// that holds the other half of this lane's pairs.
-// Elements that pass through are left alone (an infinity times sin 0 is NaN).
+// The partners of a lane's elements. `partner`: the warp lane that holds them.
 template <bool INTER>
-__device__ __forceinline__ void rotate8(float (&y)[8], const Angles& a, float dir, int partner, bool turned) {
-  float o[8];
+__device__ __forceinline__ void partner8(const uint4& raw, const F2x4& x, int partner, bool turned, F2x4& out) {
+  if (INTER) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = INTER ? y[e ^ 1] : __shfl_sync(0xffffffffu, y[e], partner);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = turned ? fmaf(o[e], dir * a.s[e], y[e] * a.c[e]) : y[e];
+    for (int i = 0; i < 4; ++i) out[i] = turned ? swap2(x[i]) : both(0.f);
+    return;
+  }
+  uint4 o;
+  o.x = __shfl_sync(0xffffffffu, raw.x, partner);
+  o.y = __shfl_sync(0xffffffffu, raw.y, partner);
+  o.z = __shfl_sync(0xffffffffu, raw.z, partner);
+  o.w = __shfl_sync(0xffffffffu, raw.w, partner);
+  if (!turned) o = make_uint4(0u, 0u, 0u, 0u);
+  unpack8(o, out);
 }
 
 template <int LANES>
@@ -120,11 +130,34 @@ __device__ __forceinline__ float group_sum(float v) {
   for (int s = LANES / 2; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
+__device__ __forceinline__ float dot8(const F2x4& a, const F2x4& b) {
+  float2 v = fmul2(a[0], b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) v = ffma2(a[i], b[i], v);
+  return v.x + v.y;
+}
 
 struct HeadView {  // [.., token, head, d] bf16, strides in elements
   const __nv_bfloat16* p;
   long long sb, sn, sh;
 };
+
+// The heads of the three tensors in chunks of kHeads that do not cross tensors.
+struct Chunks {
+  int q, kv;  // chunks of q, of k and of v each
+  __host__ __device__ int all() const { return q + 2 * kv; }
+};
+__host__ __device__ inline Chunks chunks_of(int Hq, int Hkv) {
+  return Chunks{(Hq + kHeads - 1) / kHeads, (Hkv + kHeads - 1) / kHeads};
+}
+struct HeadRange {
+  int t, h0, cnt;  // tensor (0 q, 1 k, 2 v), first head, heads
+};
+__device__ __forceinline__ HeadRange heads_of(const Chunks& ch, int chunk, int Hq, int Hkv) {
+  const int t = chunk < ch.q ? 0 : (chunk < ch.q + ch.kv ? 1 : 2);
+  const int h0 = (chunk - (t == 0 ? 0 : ch.q + (t - 1) * ch.kv)) * kHeads;
+  return HeadRange{t, h0, min(kHeads, (t == 0 ? Hq : Hkv) - h0)};
+}
 
 struct NormRopeParams {
   HeadView in[3];  // q, k, v
@@ -135,106 +168,102 @@ struct NormRopeParams {
   const int32_t* slots;      // paged only
   __nv_bfloat16* out[3];     // dense: [B, H, N, d] each; paged: q [T, Hq, d] and the two pools
   int32_t* status;
-  unsigned tokens;  // B * N, or T; tokens * chunks < 2^31
-  int N, Hq, Hkv, rd, max_pos, chunks, w_bf16;
+  unsigned tokens;  // B * N, or T
+  int N, Hq, Hkv, rd, max_pos, w_bf16;
+  Chunks ch;
   long long num_slots;
   float eps;
 };
-
-// Which tensor (0 q, 1 k, 2 v) and which of its heads is head h of a token.
-__device__ __forceinline__ int tensor_of(int& h, int Hq, int Hkv) {
-  if (h < Hq) return 0;
-  h -= Hq;
-  if (h < Hkv) return 1;
-  h -= Hkv;
-  return 2;
-}
 
 template <int D, bool INTER, bool NORM, bool PAGED>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kNrThreads / kLanes;
   const int lane = threadIdx.x & (kLanes - 1);
-  const unsigned unit = blockIdx.x * kGroups + threadIdx.x / kLanes;
-  const unsigned units = p.tokens * p.chunks;
-  const unsigned tok = unit < units ? unit / p.chunks : p.tokens - 1;  // every lane stays for the shuffles
-  const int h0 = unit < units ? (unit - tok * p.chunks) * kHeads : 0;
+  const unsigned tile = blockIdx.x / p.ch.all();
+  const HeadRange hr = heads_of(p.ch, static_cast<int>(blockIdx.x - tile * p.ch.all()), p.Hq, p.Hkv);
+  const unsigned at = tile * kGroups + threadIdx.x / kLanes;
+  const bool live = at < p.tokens;
+  const unsigned tok = live ? at : p.tokens - 1;  // every lane stays for the shuffles
   const long long token = tok, b = PAGED ? 0 : tok / p.N;
   const int n = static_cast<int>(token - b * p.N);
-  const int heads = p.Hq + 2 * p.Hkv;
 
+  const HeadView& v = p.in[hr.t];
+  const __nv_bfloat16* src = v.p + b * v.sb + static_cast<long long>(PAGED ? tok : n) * v.sn + hr.h0 * v.sh;
   uint4 raw[kHeads];
 #pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    int h = h0 + i;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < heads) {
-      const int t = tensor_of(h, p.Hq, p.Hkv);
-      const HeadView& v = p.in[t];
-      const long long row = PAGED ? token * v.sn : b * v.sb + static_cast<long long>(n) * v.sn;
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(v.p + row + h * v.sh) + lane);
-    }
-  }
+  for (int i = 0; i < kHeads; ++i)
+    if (i < hr.cnt) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + i * v.sh) + lane);
+    else raw[i] = make_uint4(0u, 0u, 0u, 0u);
+
   const long long m = p.positions != nullptr ? __ldg(p.positions + token) : n;
   const bool bad = m < 0 || m >= p.max_pos;
-  Angles a;
-  load_angles<INTER>(p.cos_t, p.sin_t, bad ? 0 : m, p.rd, lane, a);
-  long long slot = -1;
-  bool bad_slot = false;
-  if (PAGED && h0 + kHeads > p.Hq) {
-    slot = __ldg(p.slots + token);
-    bad_slot = slot < -1 || slot >= p.num_slots;
+  bool write = live, bad_slot = false;
+  __nv_bfloat16* dst;
+  long long step;  // between heads
+  if (!PAGED) {
+    const int H = hr.t == 0 ? p.Hq : p.Hkv;
+    dst = p.out[hr.t] + ((b * H + hr.h0) * p.N + n) * D;
+    step = static_cast<long long>(p.N) * D;
+  } else {
+    step = D;
+    if (hr.t == 0) {
+      dst = p.out[0] + (token * p.Hq + hr.h0) * D;
+    } else {
+      const long long slot = __ldg(p.slots + token);
+      bad_slot = slot < -1 || slot >= p.num_slots;
+      write = live && slot >= 0 && !bad_slot && !bad;
+      dst = p.out[hr.t] + ((write ? slot : 0) * p.Hkv + hr.h0) * D;
+    }
   }
+  if ((bad || bad_slot) && live && lane == 0 && p.status != nullptr)
+    atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
+
+  if (hr.t == 2) {  // V is carried over
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+      if (write && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = raw[i];
+    return;
+  }
+  F2x4 c, s;
+  load_angles<INTER>(p.cos_t, p.sin_t, bad ? 0 : m, p.rd, lane, 1.f, c, s);
   const int half_lanes = p.rd / 16;
   const bool turned = 8 * lane < p.rd;
-  const int partner = (threadIdx.x & 31) + (!turned ? 0 : (lane >= half_lanes ? -half_lanes : half_lanes));
-
+  const int shift = !turned ? 0 : (lane >= half_lanes ? -half_lanes : half_lanes);
+  const int partner = (threadIdx.x & 31) + shift;
+  if (NORM) {  // z = r (x (w c) + partner (its w s))
+    F2x4 w, wp;
+    load_weights(p.w[hr.t], p.w_bf16, lane, w);
+    if (!INTER) load_weights(p.w[hr.t], p.w_bf16, lane + shift, wp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = fmul2(c[i], w[i]);
+      s[i] = fmul2(s[i], INTER ? swap2(w[i]) : wp[i]);
+    }
+  }
+  if (bad) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = both(NAN);
+  }
 #pragma unroll
   for (int i = 0; i < kHeads; ++i) {
-    int h = h0 + i;
-    const bool there = unit < units && h < heads;
-    const int t = tensor_of(h, p.Hq, p.Hkv);
-    uint4 res = raw[i];
-    // a warp's groups may hold heads of different tensors: the shuffles run for all
-    float y[8];
-    unpack8(raw[i], y);
-    if (NORM) {
-      float ss = 0.f;
+    if (i >= hr.cnt) break;  // the same for the whole CTA
+    F2x4 x, xp;
+    unpack8(raw[i], x);
+    partner8<INTER>(raw[i], x, partner, turned, xp);
+    float2 r = both(1.f);
+    if (NORM) r = both(rsqrtf(group_sum<kLanes>(dot8(x, x)) * (1.f / D) + p.eps));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-      const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / D) + p.eps);
-      float w[8];
-      load_weights(p.w[t == 1 ? 1 : 0], p.w_bf16, lane, w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= r * w[e];
+    for (int e = 0; e < 4; ++e) {
+      x[e] = ffma2(xp[e], s[e], fmul2(x[e], c[e]));
+      if (NORM) x[e] = fmul2(x[e], r);
     }
-    rotate8<INTER>(y, a, 1.f, partner, turned);
-    if (t < 2) {
-      if (bad) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = NAN;
-      }
-      res = pack8(y);
-    }
-    if (!there) continue;
-    __nv_bfloat16* dst;
-    if (!PAGED) {
-      const int H = t == 0 ? p.Hq : p.Hkv;
-      dst = p.out[t] + ((b * H + h) * p.N + n) * D;
-    } else if (t == 0) {
-      dst = p.out[0] + (token * p.Hq + h) * D;
-    } else {
-      if (slot < 0 || bad_slot || bad) continue;
-      dst = p.out[t] + (slot * p.Hkv + h) * D;
-    }
-    reinterpret_cast<uint4*>(dst)[lane] = res;
+    if (write) reinterpret_cast<uint4*>(dst + i * step)[lane] = pack8(x);
   }
-  if ((bad || bad_slot) && unit < units && lane == 0 && p.status != nullptr)
-    atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
 }
 
 struct NormRopeBwdParams {
-  HeadView x[2];             // q, k (unused without norms)
+  HeadView x[2];  // q, k (unused without norms)
   const void* w[2];
   const float* cos_t;
   const float* sin_t;
@@ -242,147 +271,155 @@ struct NormRopeBwdParams {
   const __nv_bfloat16* dz[3];  // [B, H, N, d]
   __nv_bfloat16* dx[3];        // strided like the inputs
   long long dsb[3], dsn[3], dsh[3];
-  float* dw_part;  // [ctas, 2, d]
+  float* dw_part;  // a row of d for each CTA of q and k
   int32_t* status;
-  unsigned tokens;
-  int N, Hq, Hkv, rd, max_pos, chunks, w_bf16;
+  unsigned tokens, tiles;
+  int N, Hq, Hkv, rd, max_pos, w_bf16;
+  Chunks ch;
   float eps;
 };
 
+// CTA blockIdx.x keeps its heads and takes every gridDim.x / chunks-th tile of tokens.
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kNrThreads / kLanes;
-  __shared__ float dw_s[kNrThreads / 32][2][D];
+  __shared__ float dw_s[kNrThreads / 32][D];
   const int lane = threadIdx.x & (kLanes - 1);
-  const unsigned units = p.tokens * p.chunks;
-  const int heads = p.Hq + 2 * p.Hkv;
+  const int all = p.ch.all();
+  const unsigned first = blockIdx.x / all, stride = gridDim.x / all;
+  const HeadRange hr = heads_of(p.ch, static_cast<int>(blockIdx.x - first * all), p.Hq, p.Hkv);
+  const int H = hr.t == 0 ? p.Hq : p.Hkv;
+  const bool copy = hr.t == 2;
   const int half_lanes = p.rd / 16;
   const bool turned = 8 * lane < p.rd;
   const int partner = (threadIdx.x & 31) + (!turned ? 0 : (lane >= half_lanes ? -half_lanes : half_lanes));
-  float dwq[8], dwk[8], wq[8], wk[8];
+  F2x4 dw, w;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = wq[e] = wk[e] = 0.f;
-  if (NORM) {
-    load_weights(p.w[0], p.w_bf16, lane, wq);
-    load_weights(p.w[1], p.w_bf16, lane, wk);
-  }
+  for (int i = 0; i < 4; ++i) dw[i] = w[i] = both(0.f);
+  if (NORM && !copy) load_weights(p.w[hr.t], p.w_bf16, lane, w);
   bool any_bad = false;
-  for (unsigned base = blockIdx.x * kGroups; base < units; base += gridDim.x * kGroups) {
-    const unsigned unit = base + threadIdx.x / kLanes;
-    const bool live = unit < units;
-    const unsigned tok = live ? unit / p.chunks : p.tokens - 1;
-    const int h0 = live ? (unit - tok * p.chunks) * kHeads : 0;
-    const long long token = tok, b = tok / p.N;
-    const int n = static_cast<int>(token - b * p.N);
-    uint4 rx[kHeads], rz[kHeads];
+  for (unsigned tile = first; tile < p.tiles; tile += stride) {
+    const unsigned at = tile * kGroups + threadIdx.x / kLanes;
+    const bool live = at < p.tokens;
+    const unsigned tok = live ? at : p.tokens - 1;
+    const long long b = tok / p.N;
+    const int n = static_cast<int>(tok - b * p.N);
+    const __nv_bfloat16* zs = p.dz[hr.t] + ((b * H + hr.h0) * p.N + n) * D;
+    const long long zstep = static_cast<long long>(p.N) * D;
+    uint4 rz[kHeads], rx[kHeads];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      int h = h0 + i;
-      rx[i] = rz[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < heads) {
-        const int t = tensor_of(h, p.Hq, p.Hkv);
-        const int H = t == 0 ? p.Hq : p.Hkv;
-        rz[i] = __ldg(reinterpret_cast<const uint4*>(p.dz[t] + ((b * H + h) * p.N + n) * D) + lane);
-        if (NORM && t < 2)
-          rx[i] = __ldg(reinterpret_cast<const uint4*>(p.x[t].p + b * p.x[t].sb + static_cast<long long>(n) * p.x[t].sn +
-                                                       h * p.x[t].sh) + lane);
-      }
+    for (int i = 0; i < kHeads; ++i)
+      if (i < hr.cnt) rz[i] = __ldg(reinterpret_cast<const uint4*>(zs + i * zstep) + lane);
+      else rz[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (NORM && !copy) {
+      const HeadView& v = p.x[hr.t];
+      const __nv_bfloat16* xs = v.p + b * v.sb + static_cast<long long>(n) * v.sn + hr.h0 * v.sh;
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (i < hr.cnt) rx[i] = __ldg(reinterpret_cast<const uint4*>(xs + i * v.sh) + lane);
+        else rx[i] = make_uint4(0u, 0u, 0u, 0u);
     }
-    const long long m = p.positions != nullptr ? __ldg(p.positions + token) : n;
+    const long long m = p.positions != nullptr ? __ldg(p.positions + tok) : n;
     const bool bad = m < 0 || m >= p.max_pos;
     any_bad |= bad && live;
-    Angles a;
-    load_angles<INTER>(p.cos_t, p.sin_t, bad ? 0 : m, p.rd, lane, a);
+    __nv_bfloat16* dst = p.dx[hr.t] + b * p.dsb[hr.t] + static_cast<long long>(n) * p.dsn[hr.t] + hr.h0 * p.dsh[hr.t];
+    const long long step = p.dsh[hr.t];
+    if (copy) {
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (live && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = rz[i];
+      continue;
+    }
+    F2x4 c, s;
+    load_angles<INTER>(p.cos_t, p.sin_t, bad ? 0 : m, p.rd, lane, -1.f, c, s);
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c[i] = both(NAN);
+    }
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
-      int h = h0 + i;
-      const bool there = live && h < heads;
-      const int t = tensor_of(h, p.Hq, p.Hkv);
-      float g[8];
+      if (i >= hr.cnt) break;
+      F2x4 g, gp;
       unpack8(rz[i], g);
-      rotate8<INTER>(g, a, -1.f, partner, turned);
-      if (bad) {
+      partner8<INTER>(rz[i], g, partner, turned, gp);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = NAN;
-      }
+      for (int e = 0; e < 4; ++e) g[e] = ffma2(gp[e], s[e], fmul2(g[e], c[e]));
       if (NORM) {
-        float x[8];
+        F2x4 x;
         unpack8(rx[i], x);
-        float ss = 0.f;
+        const float ss = group_sum<kLanes>(dot8(x, x));
+        const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        const float r = rsqrtf(group_sum<kLanes>(ss) * (1.f / D) + p.eps);
-        float dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] *= r;  // n
-          const float d = g[e] * x[e];
-          if (there && t == 0) dwq[e] += d;
-          if (there && t == 1) dwk[e] += d;
-          const float w = t == 1 ? wk[e] : wq[e];
-          dot = fmaf(d, w, dot);
-          g[e] *= w;
+        for (int e = 0; e < 4; ++e) {
+          x[e] = fmul2(x[e], both(r));  // n
+          if (live) dw[e] = ffma2(g[e], x[e], dw[e]);
+          g[e] = fmul2(g[e], w[e]);
         }
-        dot = group_sum<kLanes>(dot) * (1.f / D);
+        const float dot = group_sum<kLanes>(dot8(g, x)) * (1.f / D);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
+        for (int e = 0; e < 4; ++e) g[e] = fmul2(ffma2(x[e], both(-dot), g[e]), both(r));
       }
-      if (!there) continue;
-      const uint4 res = t < 2 ? pack8(g) : rz[i];
-      __nv_bfloat16* dst = p.dx[t] + b * p.dsb[t] + static_cast<long long>(n) * p.dsn[t] + h * p.dsh[t];
-      reinterpret_cast<uint4*>(dst)[lane] = res;
+      if (live) reinterpret_cast<uint4*>(dst + i * step)[lane] = pack8(g);
     }
   }
   if (any_bad && lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
-  if (NORM) {
+  if (NORM && !copy) {
     // lanes with the same elements: the warp's groups, then the CTA's warps, in that order
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
 #pragma unroll
       for (int s = kLanes; s < 32; s <<= 1) {
-        dwq[e] += __shfl_xor_sync(0xffffffffu, dwq[e], s);
-        dwk[e] += __shfl_xor_sync(0xffffffffu, dwk[e], s);
+        dw[e].x += __shfl_xor_sync(0xffffffffu, dw[e].x, s);
+        dw[e].y += __shfl_xor_sync(0xffffffffu, dw[e].y, s);
       }
       if ((threadIdx.x & 31) < kLanes) {
-        dw_s[threadIdx.x >> 5][0][8 * lane + e] = dwq[e];
-        dw_s[threadIdx.x >> 5][1][8 * lane + e] = dwk[e];
+        dw_s[threadIdx.x >> 5][8 * lane + 2 * e] = dw[e].x;
+        dw_s[threadIdx.x >> 5][8 * lane + 2 * e + 1] = dw[e].y;
       }
     }
     __syncthreads();
-    if (threadIdx.x < 2 * D) {
-      float s = 0.f;
+    if (threadIdx.x < D) {
+      float sum = 0.f;
 #pragma unroll
-      for (int wp = 0; wp < kNrThreads / 32; ++wp) s += (&dw_s[wp][0][0])[threadIdx.x];
-      p.dw_part[static_cast<long long>(blockIdx.x) * 2 * D + threadIdx.x] = s;
+      for (int wp = 0; wp < kNrThreads / 32; ++wp) sum += dw_s[wp][threadIdx.x];
+      // rows of q first, then of k
+      const int chunk = static_cast<int>(blockIdx.x - first * all);
+      const long long row = hr.t == 0 ? static_cast<long long>(first) * p.ch.q + chunk
+                                      : static_cast<long long>(stride) * p.ch.q + first * p.ch.kv + (chunk - p.ch.q);
+      p.dw_part[row * D + threadIdx.x] = sum;
     }
   }
 }
 
-// dw = sum over the CTAs' partial rows: a CTA takes 32 columns, its 32 warps
-// every 32nd row each, then one warp adds the 32 sums.
+// dw = sum over the CTAs' partial rows (q's, then k's): a CTA takes 32 columns of
+// one of the two, its 32 warps every 32nd row each, then one warp adds the 32 sums.
 template <int D>
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int rows, float* dwq, float* dwk) {
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int rows_q, int rows_k, float* dwq,
+                                                            float* dwk) {
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = blockIdx.x * 32 + lane;
+  const bool is_k = blockIdx.x >= D / 32;
+  const int col = (blockIdx.x - (is_k ? D / 32 : 0)) * 32 + lane;
+  const float* from = part + (is_k ? static_cast<long long>(rows_q) * D : 0);
+  const int rows = is_k ? rows_k : rows_q;
   float v = 0.f;
-  for (int r = warp; r < rows; r += 32) v += part[static_cast<long long>(r) * 2 * D + col];
+  for (int r = warp; r < rows; r += 32) v += from[static_cast<long long>(r) * D + col];
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) t += s[i][lane];
-    (col < D ? dwq : dwk)[col < D ? col : col - D] = t;
+    (is_k ? dwk : dwq)[col] = t;
   }
 }
 
 template <int D, bool INTER, bool NORM, bool PAGED>
 int launch_fwd_t(const NormRopeParams& p, cudaStream_t stream) {
-  const long long groups = kNrThreads / (D / 8);
-  const long long blocks = (static_cast<long long>(p.tokens) * p.chunks + groups - 1) / groups;
-  norm_rope_kernel<D, INTER, NORM, PAGED><<<static_cast<unsigned>(blocks), kNrThreads, 0, stream>>>(p);
+  constexpr unsigned groups = kNrThreads / (D / 8);
+  const unsigned tiles = (p.tokens + groups - 1) / groups;
+  norm_rope_kernel<D, INTER, NORM, PAGED><<<tiles * p.ch.all(), kNrThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 template <bool PAGED>
@@ -400,23 +437,28 @@ int launch_fwd(const NormRopeParams& p, int d, int interleaved, cudaStream_t str
 }
 
 template <int D, bool INTER, bool NORM>
-int launch_bwd_t(const NormRopeBwdParams& p, int ctas, float* dwq, float* dwk, cudaStream_t stream) {
-  norm_rope_bwd_kernel<D, INTER, NORM><<<ctas, kNrThreads, 0, stream>>>(p);
+int launch_bwd_t(const NormRopeBwdParams& p, int strips, float* dwq, float* dwk, cudaStream_t stream) {
+  norm_rope_bwd_kernel<D, INTER, NORM><<<strips * p.ch.all(), kNrThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (!NORM) return ATTN_OK;
-  norm_rope_dw_kernel<D><<<2 * D / 32, 1024, 0, stream>>>(p.dw_part, ctas, dwq, dwk);
+  norm_rope_dw_kernel<D><<<2 * D / 32, 1024, 0, stream>>>(p.dw_part, strips * p.ch.q, strips * p.ch.kv, dwq, dwk);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 }  // namespace
 
-int norm_rope_chunks(int Hq, int Hkv) { return (Hq + 2 * Hkv + kHeads - 1) / kHeads; }
+int norm_rope_chunks(int Hq, int Hkv) { return chunks_of(Hq, Hkv).all(); }
 
-int norm_rope_bwd_ctas(long long tokens, int Hq, int Hkv, int d, int sms) {
+int norm_rope_bwd_strips(long long tokens, int Hq, int Hkv, int d, int sms) {
   const long long groups = kNrThreads / (d / 8);
-  const long long blocks = (tokens * norm_rope_chunks(Hq, Hkv) + groups - 1) / groups;
-  const long long most = 4LL * sms;
-  return static_cast<int>(blocks < most ? blocks : most);
+  const long long tiles = (tokens + groups - 1) / groups;
+  const int all = norm_rope_chunks(Hq, Hkv);
+  const long long most = (kBwdCtasPerSm * static_cast<long long>(sms) + all - 1) / all;
+  return static_cast<int>(tiles < most ? tiles : most);
+}
+size_t norm_rope_bwd_workspace(int strips, int Hq, int Hkv, int d) {
+  const Chunks ch = chunks_of(Hq, Hkv);
+  return static_cast<size_t>(strips) * (ch.q + ch.kv) * d * sizeof(float);
 }
 
 int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_out, const int32_t* slots,
@@ -440,7 +482,7 @@ int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_ou
   p.Hkv = a.Hkv;
   p.rd = a.rd;
   p.max_pos = a.max_pos;
-  p.chunks = norm_rope_chunks(a.Hq, a.Hkv);
+  p.ch = chunks_of(a.Hq, a.Hkv);
   p.w_bf16 = a.w_bf16;
   p.num_slots = num_slots;
   p.eps = a.eps;
@@ -450,7 +492,7 @@ int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_ou
 
 int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], void* const dx[3], const int64_t dsb[3],
                               const int64_t dsn[3], const int64_t dsh[3], float* dwq, float* dwk, float* dw_part,
-                              int ctas, int32_t* status, cudaStream_t stream) {
+                              int strips, int32_t* status, cudaStream_t stream) {
   NormRopeBwdParams p{};
   for (int t = 0; t < 2; ++t)
     p.x[t] = HeadView{static_cast<const __nv_bfloat16*>(a.x[t]), a.sb[t], a.sn[t], a.sh[t]};
@@ -469,24 +511,26 @@ int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], vo
   p.dw_part = dw_part;
   p.status = status;
   p.tokens = static_cast<unsigned>(a.B) * a.N;
+  const unsigned groups = kNrThreads / (a.d / 8);
+  p.tiles = (p.tokens + groups - 1) / groups;
   p.N = a.N;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
   p.rd = a.rd;
   p.max_pos = a.max_pos;
-  p.chunks = norm_rope_chunks(a.Hq, a.Hkv);
+  p.ch = chunks_of(a.Hq, a.Hkv);
   p.w_bf16 = a.w_bf16;
   p.eps = a.eps;
   const bool norm = a.w[0] != nullptr;
   if (a.d == 128)
-    return a.interleaved ? (norm ? launch_bwd_t<128, true, true>(p, ctas, dwq, dwk, stream)
-                                 : launch_bwd_t<128, true, false>(p, ctas, dwq, dwk, stream))
-                         : (norm ? launch_bwd_t<128, false, true>(p, ctas, dwq, dwk, stream)
-                                 : launch_bwd_t<128, false, false>(p, ctas, dwq, dwk, stream));
-  return a.interleaved ? (norm ? launch_bwd_t<64, true, true>(p, ctas, dwq, dwk, stream)
-                               : launch_bwd_t<64, true, false>(p, ctas, dwq, dwk, stream))
-                       : (norm ? launch_bwd_t<64, false, true>(p, ctas, dwq, dwk, stream)
-                               : launch_bwd_t<64, false, false>(p, ctas, dwq, dwk, stream));
+    return a.interleaved ? (norm ? launch_bwd_t<128, true, true>(p, strips, dwq, dwk, stream)
+                                 : launch_bwd_t<128, true, false>(p, strips, dwq, dwk, stream))
+                         : (norm ? launch_bwd_t<128, false, true>(p, strips, dwq, dwk, stream)
+                                 : launch_bwd_t<128, false, false>(p, strips, dwq, dwk, stream));
+  return a.interleaved ? (norm ? launch_bwd_t<64, true, true>(p, strips, dwq, dwk, stream)
+                               : launch_bwd_t<64, true, false>(p, strips, dwq, dwk, stream))
+                       : (norm ? launch_bwd_t<64, false, true>(p, strips, dwq, dwk, stream)
+                               : launch_bwd_t<64, false, false>(p, strips, dwq, dwk, stream));
 }
 
 }  // namespace attn

@@ -416,6 +416,7 @@ int attn_qk_norm_rope(const void* q, const void* k, const void* v, const int64_t
   if (!q_out || !k_out || !v_out || !aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out))
     return ATTN_ERR_INVALID_ARG;
   if (!q || !k || !v) return ATTN_ERR_INVALID_ARG;
+  if (current_sm_count(&a.sms) != ATTN_OK) return ATTN_ERR_CUDA;
   return launch_norm_rope(a, q_out, k_out, v_out, nullptr, 0, status, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -433,6 +434,7 @@ int attn_qk_norm_rope_paged(const void* q, const void* k, const void* v, const i
   if (!q || !k || !v || !positions || !slots || !q_out || !k_cache || !v_cache || num_blocks <= 0 || block_size <= 0)
     return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(slots)) return ATTN_ERR_INVALID_ARG;
+  if (current_sm_count(&a.sms) != ATTN_OK) return ATTN_ERR_CUDA;
   return launch_norm_rope(a, q_out, k_cache, v_cache, slots, static_cast<long long>(num_blocks) * block_size, status,
                           reinterpret_cast<cudaStream_t>(stream));
 }
@@ -468,9 +470,8 @@ int attn_qk_norm_rope_backward(const void* q, const void* k, const int64_t* stri
     sb[t] = grad_strides[3 * t], sn[t] = grad_strides[3 * t + 1], sh[t] = grad_strides[3 * t + 2];
     if (sb[t] % 8 != 0 || sn[t] % 8 != 0 || sh[t] % 8 != 0) return ATTN_ERR_INVALID_ARG;
   }
-  int sms = 0;
-  if (current_sm_count(&sms) != ATTN_OK) return ATTN_ERR_CUDA;
-  const int strips = norm_rope_bwd_strips(static_cast<long long>(B) * N, Hq, Hkv, d, sms);
+  if (current_sm_count(&a.sms) != ATTN_OK) return ATTN_ERR_CUDA;
+  const int strips = norm_rope_bwd_strips(static_cast<long long>(B) * N, Hq, Hkv, d, a.sms);
   if (norm &&
       (!workspace || !aligned16(workspace) || workspace_bytes < norm_rope_bwd_workspace(strips, Hq, Hkv, d)))
     return ATTN_ERR_WORKSPACE;

@@ -138,7 +138,7 @@ struct NormRopeArgs {
   int w_bf16;
   const float *cos_t, *sin_t;
   const int32_t* positions;
-  int B, N, Hq, Hkv, d, rd, max_pos, interleaved;
+  int B, N, Hq, Hkv, d, rd, max_pos, interleaved, sms;
   float eps;
 };
 int norm_rope_chunks(int Hq, int Hkv);  // groups of head rows per token

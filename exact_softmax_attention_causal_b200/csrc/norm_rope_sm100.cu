@@ -46,6 +46,7 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kHeads = 4;  // head rows a group has in flight
+constexpr int kFwdCtasPerSm = 8;
 constexpr int kBwdCtasPerSm = 4;
 
 using F2x4 = float2[4];  // a lane's 8 elements
@@ -169,96 +170,108 @@ struct NormRopeParams {
   __nv_bfloat16* out[3];     // dense: [B, H, N, d] each; paged: q [T, Hq, d] and the two pools
   int32_t* status;
   unsigned tokens;  // B * N, or T
-  int N, Hq, Hkv, rd, max_pos, w_bf16;
+  int N, Hq, Hkv, rd, max_pos, w_bf16, parts;
   Chunks ch;
   long long num_slots;
   float eps;
 };
 
+// CTA blockIdx.x: a tile of tokens, and of the chunks the part [all part / parts, all (part + 1) / parts).
 template <int D, bool INTER, bool NORM, bool PAGED>
 __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kNrThreads / kLanes;
   const int lane = threadIdx.x & (kLanes - 1);
-  const unsigned tile = blockIdx.x / p.ch.all();
-  const HeadRange hr = heads_of(p.ch, static_cast<int>(blockIdx.x - tile * p.ch.all()), p.Hq, p.Hkv);
+  const unsigned tile = blockIdx.x / p.parts;
+  const int part = static_cast<int>(blockIdx.x - tile * p.parts), all = p.ch.all();
+  const int c_end = all * (part + 1) / p.parts;
   const unsigned at = tile * kGroups + threadIdx.x / kLanes;
   const bool live = at < p.tokens;
   const unsigned tok = live ? at : p.tokens - 1;  // every lane stays for the shuffles
   const long long token = tok, b = PAGED ? 0 : tok / p.N;
   const int n = static_cast<int>(token - b * p.N);
-
-  const HeadView& v = p.in[hr.t];
-  const __nv_bfloat16* src = v.p + b * v.sb + static_cast<long long>(PAGED ? tok : n) * v.sn + hr.h0 * v.sh;
-  uint4 raw[kHeads];
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i)
-    if (i < hr.cnt) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + i * v.sh) + lane);
-    else raw[i] = make_uint4(0u, 0u, 0u, 0u);
-
   const long long m = p.positions != nullptr ? __ldg(p.positions + token) : n;
   const bool bad = m < 0 || m >= p.max_pos;
-  bool write = live, bad_slot = false;
-  __nv_bfloat16* dst;
-  long long step;  // between heads
-  if (!PAGED) {
-    const int H = hr.t == 0 ? p.Hq : p.Hkv;
-    dst = p.out[hr.t] + ((b * H + hr.h0) * p.N + n) * D;
-    step = static_cast<long long>(p.N) * D;
-  } else {
-    step = D;
-    if (hr.t == 0) {
-      dst = p.out[0] + (token * p.Hq + hr.h0) * D;
-    } else {
-      const long long slot = __ldg(p.slots + token);
-      bad_slot = slot < -1 || slot >= p.num_slots;
-      write = live && slot >= 0 && !bad_slot && !bad;
-      dst = p.out[hr.t] + ((write ? slot : 0) * p.Hkv + hr.h0) * D;
-    }
+  long long slot = -1;
+  bool bad_slot = false;
+  if (PAGED) {
+    slot = __ldg(p.slots + token);
+    bad_slot = slot < -1 || slot >= p.num_slots;
+    if (bad_slot || bad) slot = -1;
   }
   if ((bad || bad_slot) && live && lane == 0 && p.status != nullptr)
     atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
-
-  if (hr.t == 2) {  // V is carried over
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-      if (write && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = raw[i];
-    return;
-  }
-  F2x4 c, s;
-  load_angles<INTER>(p.cos_t, p.sin_t, bad ? 0 : m, p.rd, lane, 1.f, c, s);
   const int half_lanes = p.rd / 16;
   const bool turned = 8 * lane < p.rd;
   const int shift = !turned ? 0 : (lane >= half_lanes ? -half_lanes : half_lanes);
   const int partner = (threadIdx.x & 31) + shift;
-  if (NORM) {  // z = r (x (w c) + partner (its w s))
-    F2x4 w, wp;
-    load_weights(p.w[hr.t], p.w_bf16, lane, w);
-    if (!INTER) load_weights(p.w[hr.t], p.w_bf16, lane + shift, wp);
+  F2x4 c, s;
+  int loaded = -1;  // the tensor whose weights c and s hold
+
+  for (int chunk = all * part / p.parts; chunk < c_end; ++chunk) {
+    const HeadRange hr = heads_of(p.ch, chunk, p.Hq, p.Hkv);
+    const HeadView& v = p.in[hr.t];
+    const __nv_bfloat16* src = v.p + b * v.sb + static_cast<long long>(PAGED ? tok : n) * v.sn + hr.h0 * v.sh;
+    uint4 raw[kHeads];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = fmul2(c[i], w[i]);
-      s[i] = fmul2(s[i], INTER ? swap2(w[i]) : wp[i]);
+    for (int i = 0; i < kHeads; ++i)
+      if (i < hr.cnt) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + i * v.sh) + lane);
+      else raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    bool write = live;
+    __nv_bfloat16* dst;
+    long long step;  // between heads
+    if (!PAGED) {
+      const int H = hr.t == 0 ? p.Hq : p.Hkv;
+      dst = p.out[hr.t] + ((b * H + hr.h0) * p.N + n) * D;
+      step = static_cast<long long>(p.N) * D;
+    } else {
+      step = D;
+      if (hr.t == 0) {
+        dst = p.out[0] + (token * p.Hq + hr.h0) * D;
+      } else {
+        write = live && slot >= 0;
+        dst = p.out[hr.t] + ((write ? slot : 0) * p.Hkv + hr.h0) * D;
+      }
     }
-  }
-  if (bad) {
+    if (hr.t == 2) {  // V is carried over
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = both(NAN);
-  }
-#pragma unroll
-  for (int i = 0; i < kHeads; ++i) {
-    if (i >= hr.cnt) break;  // the same for the whole CTA
-    F2x4 x, xp;
-    unpack8(raw[i], x);
-    partner8<INTER>(raw[i], x, partner, turned, xp);
-    float2 r = both(1.f);
-    if (NORM) r = both(rsqrtf(group_sum<kLanes>(dot8(x, x)) * (1.f / D) + p.eps));
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = ffma2(xp[e], s[e], fmul2(x[e], c[e]));
-      if (NORM) x[e] = fmul2(x[e], r);
+      for (int i = 0; i < kHeads; ++i)
+        if (write && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = raw[i];
+      continue;
     }
-    if (write) reinterpret_cast<uint4*>(dst + i * step)[lane] = pack8(x);
+    if (loaded < 0 || (NORM && loaded != hr.t)) {
+      loaded = hr.t;
+      load_angles<INTER>(p.cos_t, p.sin_t, bad ? 0 : m, p.rd, lane, 1.f, c, s);
+      if (NORM) {  // z = r (x (w c) + partner (its w s))
+        F2x4 w, wp;
+        load_weights(p.w[hr.t], p.w_bf16, lane, w);
+        if (!INTER) load_weights(p.w[hr.t], p.w_bf16, lane + shift, wp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          c[i] = fmul2(c[i], w[i]);
+          s[i] = fmul2(s[i], INTER ? swap2(w[i]) : wp[i]);
+        }
+      }
+      if (bad) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = both(NAN);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      if (i >= hr.cnt) break;  // the same for the whole CTA
+      F2x4 x, xp;
+      unpack8(raw[i], x);
+      partner8<INTER>(raw[i], x, partner, turned, xp);
+      float2 r = both(1.f);
+      if (NORM) r = both(rsqrtf(group_sum<kLanes>(dot8(x, x)) * (1.f / D) + p.eps));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = ffma2(xp[e], s[e], fmul2(x[e], c[e]));
+        if (NORM) x[e] = fmul2(x[e], r);
+      }
+      if (write) reinterpret_cast<uint4*>(dst + i * step)[lane] = pack8(x);
+    }
   }
 }
 
@@ -416,24 +429,29 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, i
 }
 
 template <int D, bool INTER, bool NORM, bool PAGED>
-int launch_fwd_t(const NormRopeParams& p, cudaStream_t stream) {
+int launch_fwd_t(NormRopeParams p, int sms, cudaStream_t stream) {
   constexpr unsigned groups = kNrThreads / (D / 8);
   const unsigned tiles = (p.tokens + groups - 1) / groups;
-  norm_rope_kernel<D, INTER, NORM, PAGED><<<tiles * p.ch.all(), kNrThreads, 0, stream>>>(p);
+  // As many heads a CTA as leave kFwdCtasPerSm CTAs for every SM: angles and
+  // weights are then read once for all of them.
+  const unsigned parts = (kFwdCtasPerSm * static_cast<unsigned>(sms) + tiles - 1) / tiles;
+  const unsigned all = p.ch.all();
+  p.parts = static_cast<int>(parts < all ? parts : all);
+  norm_rope_kernel<D, INTER, NORM, PAGED><<<tiles * p.parts, kNrThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 template <bool PAGED>
-int launch_fwd(const NormRopeParams& p, int d, int interleaved, cudaStream_t stream) {
+int launch_fwd(const NormRopeParams& p, int d, int interleaved, int sms, cudaStream_t stream) {
   const bool norm = p.w[0] != nullptr;
   if (d == 128)
-    return interleaved ? (norm ? launch_fwd_t<128, true, true, PAGED>(p, stream)
-                               : launch_fwd_t<128, true, false, PAGED>(p, stream))
-                       : (norm ? launch_fwd_t<128, false, true, PAGED>(p, stream)
-                               : launch_fwd_t<128, false, false, PAGED>(p, stream));
-  return interleaved ? (norm ? launch_fwd_t<64, true, true, PAGED>(p, stream)
-                             : launch_fwd_t<64, true, false, PAGED>(p, stream))
-                     : (norm ? launch_fwd_t<64, false, true, PAGED>(p, stream)
-                             : launch_fwd_t<64, false, false, PAGED>(p, stream));
+    return interleaved ? (norm ? launch_fwd_t<128, true, true, PAGED>(p, sms, stream)
+                               : launch_fwd_t<128, true, false, PAGED>(p, sms, stream))
+                       : (norm ? launch_fwd_t<128, false, true, PAGED>(p, sms, stream)
+                               : launch_fwd_t<128, false, false, PAGED>(p, sms, stream));
+  return interleaved ? (norm ? launch_fwd_t<64, true, true, PAGED>(p, sms, stream)
+                             : launch_fwd_t<64, true, false, PAGED>(p, sms, stream))
+                     : (norm ? launch_fwd_t<64, false, true, PAGED>(p, sms, stream)
+                             : launch_fwd_t<64, false, false, PAGED>(p, sms, stream));
 }
 
 template <int D, bool INTER, bool NORM>
@@ -486,8 +504,8 @@ int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_ou
   p.w_bf16 = a.w_bf16;
   p.num_slots = num_slots;
   p.eps = a.eps;
-  return slots != nullptr ? launch_fwd<true>(p, a.d, a.interleaved, stream)
-                          : launch_fwd<false>(p, a.d, a.interleaved, stream);
+  return slots != nullptr ? launch_fwd<true>(p, a.d, a.interleaved, a.sms, stream)
+                          : launch_fwd<false>(p, a.d, a.interleaved, a.sms, stream);
 }
 
 int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], void* const dx[3], const int64_t dsb[3],

@@ -47,7 +47,7 @@ namespace {
 constexpr int kNrThreads = 256;
 constexpr int kHeads = 4;  // head rows a group has in flight
 constexpr int kFwdCtasPerSm = 8;
-constexpr int kBwdCtasPerSm = 4;
+constexpr int kBwdCtasPerSm = 2;
 
 using F2x4 = float2[4];  // a lane's 8 elements
 
@@ -284,33 +284,32 @@ struct NormRopeBwdParams {
   const __nv_bfloat16* dz[3];  // [B, H, N, d]
   __nv_bfloat16* dx[3];        // strided like the inputs
   long long dsb[3], dsn[3], dsh[3];
-  float* dw_part;  // a row of d for each CTA of q and k
+  float* dw_part;  // a row of d for each CTA and weight: [2][gridDim.x][d]
   int32_t* status;
   unsigned tokens, tiles;
-  int N, Hq, Hkv, rd, max_pos, w_bf16;
+  int N, Hq, Hkv, rd, max_pos, w_bf16, parts;
   Chunks ch;
   float eps;
 };
 
-// CTA blockIdx.x keeps its heads and takes every gridDim.x / chunks-th tile of tokens.
+// CTA blockIdx.x: of the chunks a part, as in the forward pass, for every
+// (gridDim.x / parts)-th tile of tokens. Two CTAs an SM: a third would leave 85
+// registers a thread, which the rows in flight and the weight sums do not fit.
 template <int D, bool INTER, bool NORM>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
+__global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kNrThreads / kLanes;
   __shared__ float dw_s[kNrThreads / 32][D];
   const int lane = threadIdx.x & (kLanes - 1);
-  const int all = p.ch.all();
-  const unsigned first = blockIdx.x / all, stride = gridDim.x / all;
-  const HeadRange hr = heads_of(p.ch, static_cast<int>(blockIdx.x - first * all), p.Hq, p.Hkv);
-  const int H = hr.t == 0 ? p.Hq : p.Hkv;
-  const bool copy = hr.t == 2;
+  const unsigned first = blockIdx.x / p.parts, stride = gridDim.x / p.parts;
+  const int part = static_cast<int>(blockIdx.x - first * p.parts), all = p.ch.all();
+  const int c_begin = all * part / p.parts, c_end = all * (part + 1) / p.parts;
   const int half_lanes = p.rd / 16;
   const bool turned = 8 * lane < p.rd;
   const int partner = (threadIdx.x & 31) + (!turned ? 0 : (lane >= half_lanes ? -half_lanes : half_lanes));
-  F2x4 dw, w;
+  F2x4 dwq, dwk;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dw[i] = w[i] = both(0.f);
-  if (NORM && !copy) load_weights(p.w[hr.t], p.w_bf16, lane, w);
+  for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = both(0.f);
   bool any_bad = false;
   for (unsigned tile = first; tile < p.tiles; tile += stride) {
     const unsigned at = tile * kGroups + threadIdx.x / kLanes;
@@ -318,89 +317,104 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRop
     const unsigned tok = live ? at : p.tokens - 1;
     const long long b = tok / p.N;
     const int n = static_cast<int>(tok - b * p.N);
-    const __nv_bfloat16* zs = p.dz[hr.t] + ((b * H + hr.h0) * p.N + n) * D;
-    const long long zstep = static_cast<long long>(p.N) * D;
-    uint4 rz[kHeads], rx[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-      if (i < hr.cnt) rz[i] = __ldg(reinterpret_cast<const uint4*>(zs + i * zstep) + lane);
-      else rz[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (NORM && !copy) {
-      const HeadView& v = p.x[hr.t];
-      const __nv_bfloat16* xs = v.p + b * v.sb + static_cast<long long>(n) * v.sn + hr.h0 * v.sh;
-#pragma unroll
-      for (int i = 0; i < kHeads; ++i)
-        if (i < hr.cnt) rx[i] = __ldg(reinterpret_cast<const uint4*>(xs + i * v.sh) + lane);
-        else rx[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
     const long long m = p.positions != nullptr ? __ldg(p.positions + tok) : n;
     const bool bad = m < 0 || m >= p.max_pos;
     any_bad |= bad && live;
-    __nv_bfloat16* dst = p.dx[hr.t] + b * p.dsb[hr.t] + static_cast<long long>(n) * p.dsn[hr.t] + hr.h0 * p.dsh[hr.t];
-    const long long step = p.dsh[hr.t];
-    if (copy) {
-#pragma unroll
-      for (int i = 0; i < kHeads; ++i)
-        if (live && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = rz[i];
-      continue;
-    }
     F2x4 c, s;
     load_angles<INTER>(p.cos_t, p.sin_t, bad ? 0 : m, p.rd, lane, -1.f, c, s);
     if (bad) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[i] = both(NAN);
     }
+    for (int chunk = c_begin; chunk < c_end; ++chunk) {
+      const HeadRange hr = heads_of(p.ch, chunk, p.Hq, p.Hkv);
+      const bool copy = hr.t == 2;
+      const __nv_bfloat16* zs = p.dz[hr.t] + ((b * (hr.t == 0 ? p.Hq : p.Hkv) + hr.h0) * p.N + n) * D;
+      const long long zstep = static_cast<long long>(p.N) * D;
+      uint4 rz[kHeads], rx[kHeads];
 #pragma unroll
-    for (int i = 0; i < kHeads; ++i) {
-      if (i >= hr.cnt) break;
-      F2x4 g, gp;
-      unpack8(rz[i], g);
-      partner8<INTER>(rz[i], g, partner, turned, gp);
+      for (int i = 0; i < kHeads; ++i)
+        if (i < hr.cnt) rz[i] = __ldg(reinterpret_cast<const uint4*>(zs + i * zstep) + lane);
+        else rz[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (NORM && !copy) {
+        const HeadView& v = p.x[hr.t];
+        const __nv_bfloat16* xs = v.p + b * v.sb + static_cast<long long>(n) * v.sn + hr.h0 * v.sh;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) g[e] = ffma2(gp[e], s[e], fmul2(g[e], c[e]));
-      if (NORM) {
-        F2x4 x;
-        unpack8(rx[i], x);
-        const float ss = group_sum<kLanes>(dot8(x, x));
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = fmul2(x[e], both(r));  // n
-          if (live) dw[e] = ffma2(g[e], x[e], dw[e]);
-          g[e] = fmul2(g[e], w[e]);
-        }
-        const float dot = group_sum<kLanes>(dot8(g, x)) * (1.f / D);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = fmul2(ffma2(x[e], both(-dot), g[e]), both(r));
+        for (int i = 0; i < kHeads; ++i)
+          if (i < hr.cnt) rx[i] = __ldg(reinterpret_cast<const uint4*>(xs + i * v.sh) + lane);
+          else rx[i] = make_uint4(0u, 0u, 0u, 0u);
       }
-      if (live) reinterpret_cast<uint4*>(dst + i * step)[lane] = pack8(g);
+      __nv_bfloat16* dst =
+          p.dx[hr.t] + b * p.dsb[hr.t] + static_cast<long long>(n) * p.dsn[hr.t] + hr.h0 * p.dsh[hr.t];
+      const long long step = p.dsh[hr.t];
+      if (copy) {
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+          if (live && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = rz[i];
+        continue;
+      }
+      F2x4 w, dw;
+      if (NORM) load_weights(p.w[hr.t], p.w_bf16, lane, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dw[i] = both(0.f);
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        if (i >= hr.cnt) break;
+        F2x4 g, gp;
+        unpack8(rz[i], g);
+        partner8<INTER>(rz[i], g, partner, turned, gp);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = ffma2(gp[e], s[e], fmul2(g[e], c[e]));
+        if (NORM) {
+          F2x4 x;
+          unpack8(rx[i], x);
+          const float ss = group_sum<kLanes>(dot8(x, x));
+          const float r = rsqrtf(ss * (1.f / D) + p.eps);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = fmul2(x[e], both(r));  // n
+            dw[e] = ffma2(g[e], x[e], dw[e]);
+            g[e] = fmul2(g[e], w[e]);
+          }
+          const float dot = group_sum<kLanes>(dot8(g, x)) * (1.f / D);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = fmul2(ffma2(x[e], both(-dot), g[e]), both(r));
+        }
+        if (live) reinterpret_cast<uint4*>(dst + i * step)[lane] = pack8(g);
+      }
+      if (NORM && live) {
+        F2x4& sum = hr.t == 0 ? dwq : dwk;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e] = fadd2(sum[e], dw[e]);
+      }
     }
   }
   if (any_bad && lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
-  if (NORM && !copy) {
-    // lanes with the same elements: the warp's groups, then the CTA's warps, in that order
+  if (NORM) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int t = 0; t < 2; ++t) {
+      // lanes with the same elements: the warp's groups, then the CTA's warps, in that order
+      F2x4& dw = t == 0 ? dwq : dwk;
 #pragma unroll
-      for (int s = kLanes; s < 32; s <<= 1) {
-        dw[e].x += __shfl_xor_sync(0xffffffffu, dw[e].x, s);
-        dw[e].y += __shfl_xor_sync(0xffffffffu, dw[e].y, s);
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int s = kLanes; s < 32; s <<= 1) {
+          dw[e].x += __shfl_xor_sync(0xffffffffu, dw[e].x, s);
+          dw[e].y += __shfl_xor_sync(0xffffffffu, dw[e].y, s);
+        }
+        if ((threadIdx.x & 31) < kLanes) {
+          dw_s[threadIdx.x >> 5][8 * lane + 2 * e] = dw[e].x;
+          dw_s[threadIdx.x >> 5][8 * lane + 2 * e + 1] = dw[e].y;
+        }
       }
-      if ((threadIdx.x & 31) < kLanes) {
-        dw_s[threadIdx.x >> 5][8 * lane + 2 * e] = dw[e].x;
-        dw_s[threadIdx.x >> 5][8 * lane + 2 * e + 1] = dw[e].y;
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float sum = 0.f;
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float sum = 0.f;
 #pragma unroll
-      for (int wp = 0; wp < kNrThreads / 32; ++wp) sum += dw_s[wp][threadIdx.x];
-      // rows of q first, then of k
-      const int chunk = static_cast<int>(blockIdx.x - first * all);
-      const long long row = hr.t == 0 ? static_cast<long long>(first) * p.ch.q + chunk
-                                      : static_cast<long long>(stride) * p.ch.q + first * p.ch.kv + (chunk - p.ch.q);
-      p.dw_part[row * D + threadIdx.x] = sum;
+        for (int wp = 0; wp < kNrThreads / 32; ++wp) sum += dw_s[wp][threadIdx.x];
+        p.dw_part[(static_cast<long long>(t) * gridDim.x + blockIdx.x) * D + threadIdx.x] = sum;
+      }
+      __syncthreads();
     }
   }
 }
@@ -408,14 +422,12 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NormRop
 // dw = sum over the CTAs' partial rows (q's, then k's): a CTA takes 32 columns of
 // one of the two, its 32 warps every 32nd row each, then one warp adds the 32 sums.
 template <int D>
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int rows_q, int rows_k, float* dwq,
-                                                            float* dwk) {
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int rows, float* dwq, float* dwk) {
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_k = blockIdx.x >= D / 32;
   const int col = (blockIdx.x - (is_k ? D / 32 : 0)) * 32 + lane;
-  const float* from = part + (is_k ? static_cast<long long>(rows_q) * D : 0);
-  const int rows = is_k ? rows_k : rows_q;
+  const float* from = part + (is_k ? static_cast<long long>(rows) * D : 0);
   float v = 0.f;
   for (int r = warp; r < rows; r += 32) v += from[static_cast<long long>(r) * D + col];
   s[warp][lane] = v;
@@ -455,11 +467,11 @@ int launch_fwd(const NormRopeParams& p, int d, int interleaved, int sms, cudaStr
 }
 
 template <int D, bool INTER, bool NORM>
-int launch_bwd_t(const NormRopeBwdParams& p, int strips, float* dwq, float* dwk, cudaStream_t stream) {
-  norm_rope_bwd_kernel<D, INTER, NORM><<<strips * p.ch.all(), kNrThreads, 0, stream>>>(p);
+int launch_bwd_t(const NormRopeBwdParams& p, int ctas, float* dwq, float* dwk, cudaStream_t stream) {
+  norm_rope_bwd_kernel<D, INTER, NORM><<<ctas, kNrThreads, 0, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (!NORM) return ATTN_OK;
-  norm_rope_dw_kernel<D><<<2 * D / 32, 1024, 0, stream>>>(p.dw_part, strips * p.ch.q, strips * p.ch.kv, dwq, dwk);
+  norm_rope_dw_kernel<D><<<2 * D / 32, 1024, 0, stream>>>(p.dw_part, ctas, dwq, dwk);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -467,16 +479,29 @@ int launch_bwd_t(const NormRopeBwdParams& p, int strips, float* dwq, float* dwk,
 
 int norm_rope_chunks(int Hq, int Hkv) { return chunks_of(Hq, Hkv).all(); }
 
-int norm_rope_bwd_strips(long long tokens, int Hq, int Hkv, int d, int sms) {
+// One wave of CTAs, `strips` of them side by side for each part of the heads:
+// the split that keeps most of the wave busy to the end (for 1,024 tiles on 148
+// SMs 296 strips of all heads would take 4 turns, the last one for 136 of them).
+NormRopeBwdPlan norm_rope_bwd_plan(long long tokens, int Hq, int Hkv, int d, int sms) {
   const long long groups = kNrThreads / (d / 8);
   const long long tiles = (tokens + groups - 1) / groups;
+  const long long wave = static_cast<long long>(kBwdCtasPerSm) * sms;
   const int all = norm_rope_chunks(Hq, Hkv);
-  const long long most = (kBwdCtasPerSm * static_cast<long long>(sms) + all - 1) / all;
-  return static_cast<int>(tiles < most ? tiles : most);
+  NormRopeBwdPlan best{1, 1};
+  double busy = 0.;
+  for (int parts = 1; parts <= all && parts <= wave; ++parts) {
+    const long long strips = tiles < wave / parts ? tiles : wave / parts;
+    const long long turns = (tiles + strips - 1) / strips;
+    const double share = static_cast<double>(tiles) * parts / (static_cast<double>(turns) * wave);
+    if (share > busy * 1.02) {  // more parts read the angles more often
+      busy = share;
+      best = NormRopeBwdPlan{static_cast<int>(strips), parts};
+    }
+  }
+  return best;
 }
-size_t norm_rope_bwd_workspace(int strips, int Hq, int Hkv, int d) {
-  const Chunks ch = chunks_of(Hq, Hkv);
-  return static_cast<size_t>(strips) * (ch.q + ch.kv) * d * sizeof(float);
+size_t norm_rope_bwd_workspace(const NormRopeBwdPlan& plan, int d) {
+  return static_cast<size_t>(plan.strips) * plan.parts * 2 * d * sizeof(float);
 }
 
 int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_out, const int32_t* slots,
@@ -510,8 +535,10 @@ int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_ou
 
 int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], void* const dx[3], const int64_t dsb[3],
                               const int64_t dsn[3], const int64_t dsh[3], float* dwq, float* dwk, float* dw_part,
-                              int strips, int32_t* status, cudaStream_t stream) {
+                              const NormRopeBwdPlan& plan, int32_t* status, cudaStream_t stream) {
   NormRopeBwdParams p{};
+  const int ctas = plan.strips * plan.parts;
+  p.parts = plan.parts;
   for (int t = 0; t < 2; ++t)
     p.x[t] = HeadView{static_cast<const __nv_bfloat16*>(a.x[t]), a.sb[t], a.sn[t], a.sh[t]};
   for (int t = 0; t < 3; ++t) {
@@ -541,14 +568,14 @@ int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], vo
   p.eps = a.eps;
   const bool norm = a.w[0] != nullptr;
   if (a.d == 128)
-    return a.interleaved ? (norm ? launch_bwd_t<128, true, true>(p, strips, dwq, dwk, stream)
-                                 : launch_bwd_t<128, true, false>(p, strips, dwq, dwk, stream))
-                         : (norm ? launch_bwd_t<128, false, true>(p, strips, dwq, dwk, stream)
-                                 : launch_bwd_t<128, false, false>(p, strips, dwq, dwk, stream));
-  return a.interleaved ? (norm ? launch_bwd_t<64, true, true>(p, strips, dwq, dwk, stream)
-                               : launch_bwd_t<64, true, false>(p, strips, dwq, dwk, stream))
-                       : (norm ? launch_bwd_t<64, false, true>(p, strips, dwq, dwk, stream)
-                               : launch_bwd_t<64, false, false>(p, strips, dwq, dwk, stream));
+    return a.interleaved ? (norm ? launch_bwd_t<128, true, true>(p, ctas, dwq, dwk, stream)
+                                 : launch_bwd_t<128, true, false>(p, ctas, dwq, dwk, stream))
+                         : (norm ? launch_bwd_t<128, false, true>(p, ctas, dwq, dwk, stream)
+                                 : launch_bwd_t<128, false, false>(p, ctas, dwq, dwk, stream));
+  return a.interleaved ? (norm ? launch_bwd_t<64, true, true>(p, ctas, dwq, dwk, stream)
+                               : launch_bwd_t<64, true, false>(p, ctas, dwq, dwk, stream))
+                       : (norm ? launch_bwd_t<64, false, true>(p, ctas, dwq, dwk, stream)
+                               : launch_bwd_t<64, false, false>(p, ctas, dwq, dwk, stream));
 }
 
 }  // namespace attn

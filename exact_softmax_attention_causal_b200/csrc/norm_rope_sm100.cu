@@ -21,13 +21,16 @@
 // instructions count too: pairs of elements share one (f32x2), and weights and
 // angles are multiplied once a token, not once a head.
 //
-// A group of lanes takes up to kHeads heads of one tensor of one token, their
-// loads all in flight before the first is used. The groups of a CTA take the
-// same heads of consecutive tokens: a head's rows then lie together on the
-// [B, H, N, d] side (4 KB at d = 128), a token's heads on the other (1 KB).
-// With consecutive groups on the heads of one token instead, the 256-byte rows
-// went out N rows apart: 113 us for B = 4, N = 4096, 32 / 8 heads, against FWDUS us
-// now (FWDPC % of HBM); the backward pass 168 us against BWDUS us (BWDPC %).
+// A group of lanes takes one token, and kHeads heads of one tensor at a time,
+// copied to shared memory one step ahead. The groups of a CTA take the same heads
+// of consecutive tokens: a head's rows then lie together on the [B, H, N, d] side
+// (4 KB at d = 128), a token's heads on the other (1 KB), and angles and weights
+// are read once for all heads of the CTA. Measured for B = 4, N = 4096, 32 / 8
+// heads, d = 128 (forward 405 MB, backward 573 MB): one group per 4 heads of a
+// token, groups on a token's heads 113 and 168 us; groups on consecutive tokens
+// 80 and 127; all heads of a token in turn 71 and 120; the steps prefetched 66
+// (93 % of HBM) and 107 (82 %; its two sums a row and three tensors leave 16
+// warps an SM, so latency is not hidden to the end).
 //
 // All arithmetic is in 32 bits; the result is rounded to bf16 once. The weight
 // gradients are summed in 32 bits in a fixed order: over a thread's rows, the
@@ -138,6 +141,24 @@ __device__ __forceinline__ float dot8(const F2x4& a, const F2x4& b) {
   return v.x + v.y;
 }
 
+// A thread's own ring of 16-byte pieces in shared memory: cp.async fills a step's
+// pieces kSteps - 1 steps ahead, the same thread reads them, so the loads in flight
+// cost no registers and no barrier. A step's pieces are written over those of the
+// step before the current one, whose values are long used.
+constexpr int kSteps = 2;
+template <int PIECES>
+struct Ring {
+  static constexpr int kBytes = kSteps * PIECES * kNrThreads * 16;
+  uint32_t base;
+  const uint4* mem;
+  __device__ __forceinline__ explicit Ring(uint4* smem) : base(smem_u32(smem + threadIdx.x)), mem(smem + threadIdx.x) {}
+  __device__ __forceinline__ void load(int slot, int i, const void* src) {
+    cp_async_16(base + (slot * PIECES + i) * kNrThreads * 16, src, 16);
+  }
+  __device__ __forceinline__ uint4 get(int slot, int i) const { return mem[(slot * PIECES + i) * kNrThreads]; }
+};
+__device__ __forceinline__ int next_slot(int slot) { return slot + 1 == kSteps ? 0 : slot + 1; }
+
 struct HeadView {  // [.., token, head, d] bf16, strides in elements
   const __nv_bfloat16* p;
   long long sb, sn, sh;
@@ -184,12 +205,30 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
   const int lane = threadIdx.x & (kLanes - 1);
   const unsigned tile = blockIdx.x / p.parts;
   const int part = static_cast<int>(blockIdx.x - tile * p.parts), all = p.ch.all();
-  const int c_end = all * (part + 1) / p.parts;
+  const int c_begin = all * part / p.parts, c_end = all * (part + 1) / p.parts;
   const unsigned at = tile * kGroups + threadIdx.x / kLanes;
   const bool live = at < p.tokens;
   const unsigned tok = live ? at : p.tokens - 1;  // every lane stays for the shuffles
   const long long token = tok, b = PAGED ? 0 : tok / p.N;
   const int n = static_cast<int>(token - b * p.N);
+  extern __shared__ uint4 ring_smem[];
+  Ring<kHeads> ring(ring_smem);
+  int slot_at = 0, slot_in = 0;
+  auto fetch = [&](int chunk) {
+    if (chunk < c_end) {
+      const HeadRange hr = heads_of(p.ch, chunk, p.Hq, p.Hkv);
+      const HeadView& v = p.in[hr.t];
+      const __nv_bfloat16* src =
+          v.p + b * v.sb + static_cast<long long>(PAGED ? tok : n) * v.sn + hr.h0 * v.sh + 8 * lane;
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (i < hr.cnt) ring.load(slot_in, i, src + i * v.sh);
+      slot_in = next_slot(slot_in);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kSteps - 1; ++i) fetch(c_begin + i);
   const long long m = p.positions != nullptr ? __ldg(p.positions + token) : n;
   const bool bad = m < 0 || m >= p.max_pos;
   long long slot = -1;
@@ -208,15 +247,10 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
   F2x4 c, s;
   int loaded = -1;  // the tensor whose weights c and s hold
 
-  for (int chunk = all * part / p.parts; chunk < c_end; ++chunk) {
+  for (int chunk = c_begin; chunk < c_end; ++chunk, slot_at = next_slot(slot_at)) {
     const HeadRange hr = heads_of(p.ch, chunk, p.Hq, p.Hkv);
-    const HeadView& v = p.in[hr.t];
-    const __nv_bfloat16* src = v.p + b * v.sb + static_cast<long long>(PAGED ? tok : n) * v.sn + hr.h0 * v.sh;
-    uint4 raw[kHeads];
-#pragma unroll
-    for (int i = 0; i < kHeads; ++i)
-      if (i < hr.cnt) raw[i] = __ldg(reinterpret_cast<const uint4*>(src + i * v.sh) + lane);
-      else raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    cp_async_wait<kSteps - 2>();
+    fetch(chunk + kSteps - 1);
     bool write = live;
     __nv_bfloat16* dst;
     long long step;  // between heads
@@ -236,7 +270,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
     if (hr.t == 2) {  // V is carried over
 #pragma unroll
       for (int i = 0; i < kHeads; ++i)
-        if (write && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = raw[i];
+        if (write && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = ring.get(slot_at, i);
       continue;
     }
     if (loaded < 0 || (NORM && loaded != hr.t)) {
@@ -260,9 +294,10 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       if (i >= hr.cnt) break;  // the same for the whole CTA
+      const uint4 raw = ring.get(slot_at, i);
       F2x4 x, xp;
-      unpack8(raw[i], x);
-      partner8<INTER>(raw[i], x, partner, turned, xp);
+      unpack8(raw, x);
+      partner8<INTER>(raw, x, partner, turned, xp);
       float2 r = both(1.f);
       if (NORM) r = both(rsqrtf(group_sum<kLanes>(dot8(x, x)) * (1.f / D) + p.eps));
 #pragma unroll
@@ -293,8 +328,8 @@ struct NormRopeBwdParams {
 };
 
 // CTA blockIdx.x: of the chunks a part, as in the forward pass, for every
-// (gridDim.x / parts)-th tile of tokens. Two CTAs an SM: a third would leave 85
-// registers a thread, which the rows in flight and the weight sums do not fit.
+// (gridDim.x / parts)-th tile of tokens. Two CTAs an SM: three, at 80 registers,
+// took 111 us where two take 107.
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int kLanes = D / 8;
@@ -311,12 +346,63 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
 #pragma unroll
   for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = both(0.f);
   bool any_bad = false;
-  for (unsigned tile = first; tile < p.tiles; tile += stride) {
+  struct Place {  // this thread's token of a tile
+    bool live;
+    unsigned tok;
+    long long b;
+    int n;
+  };
+  auto place = [&](unsigned tile) {
     const unsigned at = tile * kGroups + threadIdx.x / kLanes;
-    const bool live = at < p.tokens;
-    const unsigned tok = live ? at : p.tokens - 1;
-    const long long b = tok / p.N;
-    const int n = static_cast<int>(tok - b * p.N);
+    Place w;
+    w.live = at < p.tokens;
+    w.tok = w.live ? at : p.tokens - 1;
+    w.b = w.tok / p.N;
+    w.n = static_cast<int>(w.tok - w.b * p.N);
+    return w;
+  };
+  // the summing grid may be set up now; it waits for this one's end
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  extern __shared__ uint4 ring_smem[];
+  Ring<2 * kHeads> ring(ring_smem);  // dz's pieces, then x's
+  int slot_at = 0, slot_in = 0;
+  // the step to fetch next: a chunk of a tile
+  unsigned f_tile = first;
+  int f_chunk = c_begin;
+  Place fp = place(first < p.tiles ? first : 0);
+  auto fetch = [&]() {
+    if (f_tile < p.tiles) {
+      const HeadRange hr = heads_of(p.ch, f_chunk, p.Hq, p.Hkv);
+      const __nv_bfloat16* zs =
+          p.dz[hr.t] + ((fp.b * (hr.t == 0 ? p.Hq : p.Hkv) + hr.h0) * p.N + fp.n) * D + 8 * lane;
+      const long long zstep = static_cast<long long>(p.N) * D;
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (i < hr.cnt) ring.load(slot_in, i, zs + i * zstep);
+      if (NORM && hr.t < 2) {
+        const HeadView& v = p.x[hr.t];
+        const __nv_bfloat16* xs = v.p + fp.b * v.sb + static_cast<long long>(fp.n) * v.sn + hr.h0 * v.sh + 8 * lane;
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i)
+          if (i < hr.cnt) ring.load(slot_in, kHeads + i, xs + i * v.sh);
+      }
+      slot_in = next_slot(slot_in);
+      if (++f_chunk == c_end) {
+        f_chunk = c_begin;
+        f_tile += stride;
+        if (f_tile < p.tiles) fp = place(f_tile);
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kSteps - 1; ++i) fetch();
+  for (unsigned tile = first; tile < p.tiles; tile += stride) {
+    const Place pl = place(tile);
+    const bool live = pl.live;
+    const unsigned tok = pl.tok;
+    const long long b = pl.b;
+    const int n = pl.n;
     const long long m = p.positions != nullptr ? __ldg(p.positions + tok) : n;
     const bool bad = m < 0 || m >= p.max_pos;
     any_bad |= bad && live;
@@ -326,31 +412,18 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
 #pragma unroll
       for (int i = 0; i < 4; ++i) c[i] = both(NAN);
     }
-    for (int chunk = c_begin; chunk < c_end; ++chunk) {
+    for (int chunk = c_begin; chunk < c_end; ++chunk, slot_at = next_slot(slot_at)) {
       const HeadRange hr = heads_of(p.ch, chunk, p.Hq, p.Hkv);
       const bool copy = hr.t == 2;
-      const __nv_bfloat16* zs = p.dz[hr.t] + ((b * (hr.t == 0 ? p.Hq : p.Hkv) + hr.h0) * p.N + n) * D;
-      const long long zstep = static_cast<long long>(p.N) * D;
-      uint4 rz[kHeads], rx[kHeads];
-#pragma unroll
-      for (int i = 0; i < kHeads; ++i)
-        if (i < hr.cnt) rz[i] = __ldg(reinterpret_cast<const uint4*>(zs + i * zstep) + lane);
-        else rz[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (NORM && !copy) {
-        const HeadView& v = p.x[hr.t];
-        const __nv_bfloat16* xs = v.p + b * v.sb + static_cast<long long>(n) * v.sn + hr.h0 * v.sh;
-#pragma unroll
-        for (int i = 0; i < kHeads; ++i)
-          if (i < hr.cnt) rx[i] = __ldg(reinterpret_cast<const uint4*>(xs + i * v.sh) + lane);
-          else rx[i] = make_uint4(0u, 0u, 0u, 0u);
-      }
+      cp_async_wait<kSteps - 2>();
+      fetch();
       __nv_bfloat16* dst =
           p.dx[hr.t] + b * p.dsb[hr.t] + static_cast<long long>(n) * p.dsn[hr.t] + hr.h0 * p.dsh[hr.t];
       const long long step = p.dsh[hr.t];
       if (copy) {
 #pragma unroll
         for (int i = 0; i < kHeads; ++i)
-          if (live && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = rz[i];
+          if (live && i < hr.cnt) reinterpret_cast<uint4*>(dst + i * step)[lane] = ring.get(slot_at, i);
         continue;
       }
       F2x4 w, dw;
@@ -360,14 +433,15 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
 #pragma unroll
       for (int i = 0; i < kHeads; ++i) {
         if (i >= hr.cnt) break;
+        const uint4 rz = ring.get(slot_at, i);
         F2x4 g, gp;
-        unpack8(rz[i], g);
-        partner8<INTER>(rz[i], g, partner, turned, gp);
+        unpack8(rz, g);
+        partner8<INTER>(rz, g, partner, turned, gp);
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[e] = ffma2(gp[e], s[e], fmul2(g[e], c[e]));
         if (NORM) {
           F2x4 x;
-          unpack8(rx[i], x);
+          unpack8(ring.get(slot_at, kHeads + i), x);
           const float ss = group_sum<kLanes>(dot8(x, x));
           const float r = rsqrtf(ss * (1.f / D) + p.eps);
 #pragma unroll
@@ -423,6 +497,7 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
 // one of the two, its 32 warps every 32nd row each, then one warp adds the 32 sums.
 template <int D>
 __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, int rows, float* dwq, float* dwk) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partial rows are written
   __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool is_k = blockIdx.x >= D / 32;
@@ -449,7 +524,11 @@ int launch_fwd_t(NormRopeParams p, int sms, cudaStream_t stream) {
   const unsigned parts = (kFwdCtasPerSm * static_cast<unsigned>(sms) + tiles - 1) / tiles;
   const unsigned all = p.ch.all();
   p.parts = static_cast<int>(parts < all ? parts : all);
-  norm_rope_kernel<D, INTER, NORM, PAGED><<<tiles * p.parts, kNrThreads, 0, stream>>>(p);
+  constexpr int smem = Ring<kHeads>::kBytes;
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(norm_rope_kernel<D, INTER, NORM, PAGED>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  norm_rope_kernel<D, INTER, NORM, PAGED><<<tiles * p.parts, kNrThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 template <bool PAGED>
@@ -468,11 +547,26 @@ int launch_fwd(const NormRopeParams& p, int d, int interleaved, int sms, cudaStr
 
 template <int D, bool INTER, bool NORM>
 int launch_bwd_t(const NormRopeBwdParams& p, int ctas, float* dwq, float* dwk, cudaStream_t stream) {
-  norm_rope_bwd_kernel<D, INTER, NORM><<<ctas, kNrThreads, 0, stream>>>(p);
+  constexpr int smem = Ring<2 * kHeads>::kBytes;
+  if (cudaFuncSetAttribute(norm_rope_bwd_kernel<D, INTER, NORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return ATTN_ERR_CUDA;
+  norm_rope_bwd_kernel<D, INTER, NORM><<<ctas, kNrThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ERR_CUDA;
   if (!NORM) return ATTN_OK;
-  norm_rope_dw_kernel<D><<<2 * D / 32, 1024, 0, stream>>>(p.dw_part, ctas, dwq, dwk);
-  return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel<D>, static_cast<const float*>(p.dw_part), ctas, dwq, dwk) ==
+                 cudaSuccess
+             ? ATTN_OK
+             : ATTN_ERR_CUDA;
 }
 
 }  // namespace

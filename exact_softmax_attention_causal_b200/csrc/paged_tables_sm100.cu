@@ -37,6 +37,7 @@ namespace {
 constexpr int kTableThreads = 1024;
 constexpr int kTableCluster = 8;
 constexpr int kSmallWork = 4096;
+constexpr int kUnroll = 4;  // rows or entries a thread has in flight
 
 struct TableParams {
   const int32_t* seq_lens;
@@ -193,11 +194,26 @@ __global__ void __launch_bounds__(kTableThreads, 1) paged_table_kernel(const Tab
     const int given = static_cast<int>(run.b < room ? run.b : room);
     flag |= run.b > room;
     if (t0 == 0) *p.num_free_out = F0 + given;
-    for (unsigned i = t0; i < static_cast<unsigned>(given); i += step) {
-      const int b = last_at_or_below(off, p.B, static_cast<int>(i));
-      const int e = p.table[static_cast<size_t>(b) * p.max_blocks + (i - off[b])];
-      flag |= e < 0 || e >= p.num_blocks;
-      p.free_blocks[F + i] = e;
+    const unsigned n = given;
+    for (unsigned base = t0; base < n; base += kUnroll * step) {
+      int e[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const unsigned i = base + k * step;
+        e[k] = 0;
+        if (i < n) {
+          const int b = last_at_or_below(off, p.B, static_cast<int>(i));
+          e[k] = p.table[static_cast<size_t>(b) * p.max_blocks + (i - off[b])];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const unsigned i = base + k * step;
+        if (i < n) {
+          flag |= e[k] < 0 || e[k] >= p.num_blocks;
+          p.free_blocks[F + i] = e[k];
+        }
+      }
     }
   } else {
     if (t0 == 0) *p.num_free_out = F0 - taken;
@@ -215,22 +231,35 @@ __global__ void __launch_bounds__(kTableThreads, 1) paged_table_kernel(const Tab
       flag |= !good;
       p.table[static_cast<size_t>(b) * p.max_blocks + blocks_of(len[b], bs) + (i - off[b])] = good ? e : -1;
     }
-    for (unsigned t = t0; t < static_cast<unsigned>(p.max_tokens); t += step) {
-      int pos = 0, slot = -1;
-      if (t < static_cast<unsigned>(rows)) {
-        const int b = last_at_or_below(cu, p.B, static_cast<int>(t));
-        if (len[b] >= 0) {
-          pos = len[b] + (static_cast<int>(t) - cu[b]);
-          const int blk = pos / bs, have = blocks_of(len[b], bs);
-          // the block the sequence stopped in, or one handed out above
-          const int e = blk < have ? p.table[static_cast<size_t>(b) * p.max_blocks + blk]
-                                   : p.free_blocks[F - 1 - (off[b] + blk - have)];
-          if (e >= 0 && e < p.num_blocks) slot = e * bs + (pos - blk * bs);
-          else flag = true;
+    const unsigned n = p.max_tokens;
+    for (unsigned base = t0; base < n; base += kUnroll * step) {
+      int pos[kUnroll], at[kUnroll], e[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const unsigned t = base + k * step;
+        pos[k] = 0;
+        at[k] = e[k] = -1;
+        if (t < static_cast<unsigned>(rows)) {
+          const int b = last_at_or_below(cu, p.B, static_cast<int>(t));
+          if (len[b] >= 0) {
+            pos[k] = len[b] + (static_cast<int>(t) - cu[b]);
+            const int blk = pos[k] / bs, have = blocks_of(len[b], bs);
+            at[k] = pos[k] - blk * bs;
+            // the block the sequence stopped in, or one handed out above
+            e[k] = blk < have ? p.table[static_cast<size_t>(b) * p.max_blocks + blk]
+                              : p.free_blocks[F - 1 - (off[b] + blk - have)];
+          }
         }
       }
-      p.positions[t] = pos;
-      p.slots[t] = slot;
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) {
+        const unsigned t = base + k * step;
+        if (t >= n) break;
+        const bool good = e[k] >= 0 && e[k] < p.num_blocks;
+        flag |= at[k] >= 0 && !good;
+        p.positions[t] = pos[k];
+        p.slots[t] = at[k] >= 0 && good ? e[k] * bs + at[k] : -1;
+      }
     }
   }
   if (flag && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);

@@ -550,7 +550,7 @@ ATTN_API int attn_paged_release(const int32_t* seq_lens, const int32_t* finished
  * pointers (16 bytes; positions 4), strides not a multiple of 8, one weight
  * without the other, a bad size, rotary_dim or eps, max_pos < N without
  * positions; ATTN_ERR_UNSUPPORTED for d other than 64 or 128, rotary_dim not a
- * multiple of 16, or B * N * ceil((Hq + 2 Hkv) / 4) of 2^31 or more;
+ * multiple of 16, or B * N * (ceil(Hq / 4) + 2 ceil(Hkv / 4)) of 2^31 or more;
  * ATTN_ERR_CUDA when the launch fails.
  */
 ATTN_API int attn_qk_norm_rope(const void* q, const void* k, const void* v, const int64_t* strides,

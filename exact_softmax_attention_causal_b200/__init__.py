@@ -549,9 +549,9 @@ def paged_extend(seq_lens, new_lens, block_table, free_blocks, num_free, block_s
     """
     dev, B = _table_args(seq_lens, new_lens, "new_lens", block_table, free_blocks, num_free, status)
     n = max(0, int(max_tokens))
-    seq_lens_out, num_free_out, cu_q, positions, slots = _int32_outs(
-        ((seq_lens_out, "seq_lens_out", B), (num_free_out, "num_free_out", 1), (cu_q, "cu_q", B + 1),
-         (positions, "positions", n), (slots, "slots", n)), dev)
+    positions, slots, cu_q, seq_lens_out, num_free_out = _int32_outs(
+        ((positions, "positions", n), (slots, "slots", n), (cu_q, "cu_q", B + 1), (seq_lens_out, "seq_lens_out", B),
+         (num_free_out, "num_free_out", 1)), dev)
     rc = _lib.lib().attn_paged_extend(seq_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
                                       free_blocks.data_ptr(), num_free.data_ptr(), seq_lens_out.data_ptr(),
                                       num_free_out.data_ptr(), cu_q.data_ptr(), positions.data_ptr(),

@@ -37,7 +37,11 @@ namespace {
 constexpr int kTableThreads = 1024;
 constexpr int kTableCluster = 8;
 constexpr int kSmallWork = 4096;
-constexpr int kUnroll = 4;  // rows or entries a thread has in flight
+// Consecutive rows or entries of a thread where there are more than threads: one
+// bisection and one block's entry serve most (66,000 rows 13.1 -> 10.4 us). With
+// fewer each thread takes one: a decode step's rows are of 64 different sequences,
+// and four in turn took 6.9 us instead of 4.5.
+constexpr unsigned kRun = 4;
 
 struct TableParams {
   const int32_t* seq_lens;
@@ -194,24 +198,24 @@ __global__ void __launch_bounds__(kTableThreads, 1) paged_table_kernel(const Tab
     const int given = static_cast<int>(run.b < room ? run.b : room);
     flag |= run.b > room;
     if (t0 == 0) *p.num_free_out = F0 + given;
-    const unsigned n = given;
-    for (unsigned base = t0; base < n; base += kUnroll * step) {
-      int e[kUnroll];
+    const unsigned n = given, run = n <= step ? 1 : kRun;
+    for (unsigned i0 = run * t0; i0 < n; i0 += run * step) {
+      int b = last_at_or_below(off, p.B, static_cast<int>(i0)), e[kRun];
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const unsigned i = base + k * step;
+      for (unsigned k = 0; k < kRun; ++k) {
+        const unsigned i = i0 + k;
         e[k] = 0;
-        if (i < n) {
-          const int b = last_at_or_below(off, p.B, static_cast<int>(i));
+        if (k < run && i < n) {
+          // of equal starts the last: sequences that give nothing are passed over
+          while (b + 1 < p.B && static_cast<unsigned>(off[b + 1]) <= i) ++b;
           e[k] = p.table[static_cast<size_t>(b) * p.max_blocks + (i - off[b])];
         }
       }
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const unsigned i = base + k * step;
-        if (i < n) {
+      for (unsigned k = 0; k < kRun; ++k) {
+        if (k < run && i0 + k < n) {
           flag |= e[k] < 0 || e[k] >= p.num_blocks;
-          p.free_blocks[F + i] = e[k];
+          p.free_blocks[F + i0 + k] = e[k];
         }
       }
     }
@@ -231,34 +235,56 @@ __global__ void __launch_bounds__(kTableThreads, 1) paged_table_kernel(const Tab
       flag |= !good;
       p.table[static_cast<size_t>(b) * p.max_blocks + blocks_of(len[b], bs) + (i - off[b])] = good ? e : -1;
     }
-    const unsigned n = p.max_tokens;
-    for (unsigned base = t0; base < n; base += kUnroll * step) {
-      int pos[kUnroll], at[kUnroll], e[kUnroll];
+    const unsigned n = p.max_tokens, filled = rows, run = n <= step ? 1 : kRun;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15u) == 0;
+    for (unsigned r0 = run * t0; r0 < n; r0 += run * step) {
+      int pos[kRun], slot[kRun];
+      int b = -1, m = 0, blk = 0, at = 0, have = 0, e = -1;  // the row's sequence, position, block and its entry
+      unsigned end = 0;                                      // the sequence's last row
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const unsigned t = base + k * step;
+      for (unsigned k = 0; k < kRun; ++k) {
+        const unsigned t = r0 + k;
         pos[k] = 0;
-        at[k] = e[k] = -1;
-        if (t < static_cast<unsigned>(rows)) {
-          const int b = last_at_or_below(cu, p.B, static_cast<int>(t));
-          if (len[b] >= 0) {
-            pos[k] = len[b] + (static_cast<int>(t) - cu[b]);
-            const int blk = pos[k] / bs, have = blocks_of(len[b], bs);
-            at[k] = pos[k] - blk * bs;
-            // the block the sequence stopped in, or one handed out above
-            e[k] = blk < have ? p.table[static_cast<size_t>(b) * p.max_blocks + blk]
-                              : p.free_blocks[F - 1 - (off[b] + blk - have)];
+        slot[k] = -1;
+        if (k >= run || t >= filled) continue;
+        bool look = true;
+        if (t >= end) {
+          if (b < 0) b = last_at_or_below(cu, p.B, static_cast<int>(t));
+          while (b + 1 < p.B && static_cast<unsigned>(cu[b + 1]) <= t) ++b;
+          end = b + 1 < p.B ? cu[b + 1] : rows;
+          m = len[b] + (static_cast<int>(t) - cu[b]);
+          have = len[b] < 0 ? 0 : blocks_of(len[b], bs);
+          blk = m / bs;
+          at = m - blk * bs;
+        } else {
+          ++m;
+          look = ++at == bs;
+          if (look) {
+            at = 0;
+            ++blk;
           }
         }
+        if (len[b] < 0) continue;
+        // the block the sequence stopped in, or one handed out above
+        if (look)
+          e = blk < have ? p.table[static_cast<size_t>(b) * p.max_blocks + blk]
+                         : p.free_blocks[F - 1 - (off[b] + blk - have)];
+        const bool good = e >= 0 && e < p.num_blocks;
+        flag |= !good;
+        pos[k] = m;
+        slot[k] = good ? e * bs + at : -1;
       }
+      if (wide && run == kRun && r0 + kRun <= n) {
+        *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        *reinterpret_cast<int4*>(p.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      } else {
 #pragma unroll
-      for (int k = 0; k < kUnroll; ++k) {
-        const unsigned t = base + k * step;
-        if (t >= n) break;
-        const bool good = e[k] >= 0 && e[k] < p.num_blocks;
-        flag |= at[k] >= 0 && !good;
-        p.positions[t] = pos[k];
-        p.slots[t] = at[k] >= 0 && good ? e[k] * bs + at[k] : -1;
+        for (unsigned k = 0; k < kRun; ++k) {
+          if (k < run && r0 + k < n) {
+            p.positions[r0 + k] = pos[k];
+            p.slots[r0 + k] = slot[k];
+          }
+        }
       }
     }
   }

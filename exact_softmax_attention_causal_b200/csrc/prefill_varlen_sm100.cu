@@ -591,21 +591,16 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         if (nt == 0) break;
         if (k_warp && lane == 0) bad_s[flag] = 0;
         __syncwarp();
-        auto fetch = [&](int j) -> int {
+        // this lane's block of key tile j: whether it is asked for, and its raw entry,
+        // which nothing looks at before the next tile's turn
+        bool asked = false;
+        int raw = 0;
+        auto fetch = [&](int j) {
           const int key = gm.tile_key(pc.j0 + j) + lane * bs;
-          const bool seen = lane < boxes && key < gm.key_end && (key + bs > gm.key_lo || key < gm.sink_end);
-          int ent = p.num_blocks;
-          if (seen) {
-            ent = __ldg(p.block_table + static_cast<size_t>(pc.b) * p.max_blocks + key / bs);
-            if (ent < 0 || ent >= p.num_blocks) {
-              ent = p.num_blocks;
-              if (k_warp) bad_s[flag] = 1;
-            }
-          }
-          __syncwarp();
-          return ent;
+          asked = j < nt && lane < boxes && key < gm.key_end && (key + bs > gm.key_lo || key < gm.sink_end);
+          if (asked) raw = __ldg(p.block_table + static_cast<size_t>(pc.b) * p.max_blocks + key / bs);
         };
-        int ent = fetch(0);
+        fetch(0);
         // The second Q tile's place is a V slot of narrow items: the item before has
         // read its Q, and a wide item's Q waits for the slot's last V tile.
         bool armed = true;
@@ -630,7 +625,13 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         if (!ok) break;
         vr.enter(gm.wide);
         for (int i = 0; i < nt; ++i) {
-          const int next = i + 1 < nt ? fetch(i + 1) : p.num_blocks;
+          int ent = p.num_blocks;
+          if (asked) {
+            if (raw >= 0 && raw < p.num_blocks) ent = raw;
+            else if (k_warp) bad_s[flag] = 1;
+          }
+          fetch(i + 1);
+          __syncwarp();
           if (k_warp) {
             const int gi = g + i, s = gi % C::kStages, rnd = gi / C::kStages;
             if (lane == 0) {
@@ -675,7 +676,6 @@ __global__ void __launch_bounds__(kVlThreads, 1)
               }
             }
           }
-          ent = next;
         }
         if (!ok) {
           ++it;  // this item's Q is in flight

@@ -459,6 +459,9 @@ __global__ void __launch_bounds__(kVlThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
+  for (int i = threadIdx.x; i < C::kTile / 16; i += kVlThreads)
+    reinterpret_cast<uint4*>(smem + C::kQOff)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
   if (warp == kVlMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
@@ -610,19 +613,29 @@ __global__ void __launch_bounds__(kVlThreads, 1)
             if (armed && gm.wide)
               armed = mbar_wait_bounded(bar(kVbVEmpty + C::kStages), vr.phase(C::kStages) ^ 1u, budget, abort_flag);
             if (armed) {
-              // two boxes: both tiles of a wide item, or the same 64 rows twice
-              const int boxes_q = gm.wide || pc.half ? 2 : 1, tokens = pc.half ? p.tph : p.tpt;
-              mbar_arrive_expect_tx(bar(kVbQFull), boxes_q * C::kHalves * p.gsz * tokens * 128);
-              for (int x = 0; x < boxes_q; ++x)
-                for (int hh = 0; hh < C::kHalves; ++hh)
-                  tma_load_3d(sbase + C::kQOff + x * (pc.half ? 64 * 128 : C::kTile) + hh * C::kHalf,
-                              pc.half ? &tm_qh : &tm_q, bar(kVbQFull), hh * 64, pc.head0,
-                              pc.row0 + (pc.half ? 0 : x * p.tpt));
+              const int tiles = gm.wide ? 2 : 1;
+              const int rows = pc.half ? 2 * gm.ntok * p.gsz : tiles * p.tpt * p.gsz;
+              mbar_arrive_expect_tx(bar(kVbQFull), rows * C::kHalves * 128);
+              if (!pc.half)
+                for (int x = 0; x < tiles; ++x)
+                  for (int hh = 0; hh < C::kHalves; ++hh)
+                    tma_load_3d(sbase + C::kQOff + x * C::kTile + hh * C::kHalf, &tm_q, bar(kVbQFull), hh * 64,
+                                pc.head0, pc.row0 + x * p.tpt);
             }
           }
         }
         ok = __shfl_sync(0xffffffffu, armed, 0);
         if (!ok) break;
+        if (k_warp && pc.half) {
+          // the same rows for both teams, token by token: the tile's other rows stay as
+          // they were, zeros unless a larger item came before (zeros cost less power)
+          __syncwarp();
+          for (int t = lane; t < 2 * C::kHalves * gm.ntok; t += 32) {
+            const int tk = t / (2 * C::kHalves), x = t & 1, hh = (t >> 1) & (C::kHalves - 1);
+            tma_load_3d(sbase + C::kQOff + x * 64 * 128 + hh * C::kHalf + tk * p.gsz * 128, &tm_qh, bar(kVbQFull), hh * 64,
+                        pc.head0, pc.row0 + tk);
+          }
+        }
         vr.enter(gm.wide);
         for (int i = 0; i < nt; ++i) {
           int ent = p.num_blocks;
@@ -1149,9 +1162,8 @@ int launch_varlen_t(const VarlenArgs& a, cudaStream_t stream) {
   p.scale_log2 = a.scale * kLog2e;
   p.budget = wait_budget_cycles();
   CUtensorMap tq, tqh, tk, tv, tvr, to;
-  // maps that no piece uses (no 64-row form, no output box) stand for themselves
   if (!encode_packed(&tq, a.q, D, a.Hq, a.T, p.gsz, p.tpt) ||
-      !encode_packed(&tqh, a.q, D, a.Hq, a.T, p.gsz, p.tph > 0 ? p.tph : 1) ||
+      !encode_packed(&tqh, a.q, D, a.Hq, a.T, p.gsz, 1) ||
       !encode_packed(&to, a.o, D, a.Hq, a.T, p.gsz, p.tma_out ? 32 / p.gsz : 1) ||
       !encode_pool(&tk, a.k_cache, D, a.Hkv, a.block_size, a.num_blocks, a.block_size) ||
       !encode_pool(&tv, a.v_cache, D, a.Hkv, a.block_size, a.num_blocks, a.block_size) ||

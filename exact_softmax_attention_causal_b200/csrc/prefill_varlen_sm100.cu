@@ -66,7 +66,7 @@ constexpr float kVlRescale = 8.0f;  // base 2: the maximum moves only past this 
 // What a key costs on the line, and what an item costs besides, in proportion to
 // the cycles measured: a wide tile of 128 keys 3,650 (d = 128) and 3,300 (d = 64),
 // a narrow one COSTN, an item's ends 5,000.
-constexpr int kCostWide = 20, kCostItem = 28 * kBN;
+constexpr int kCostWide = 20, kCostItem = 28 * kBN, kCostItemNarrow = 48 * kBN;
 template <int D>
 constexpr int kCostNarrow = D == 128 ? 11 : 8;
 // A CTA's stretch holds a tile at least (a piece of every item it passes through).
@@ -203,8 +203,8 @@ __device__ __forceinline__ long long line_of(const VarlenParams& p, int n, int n
     keys = F0 * pos0 + S * (F0 * (F0 + 1) / 2) + (F - F0) * (S + W - 1) + F * extra;
     tail_keys = min(nk, tail + W - 1) + extra;
   }
-  long long c = R * static_cast<long long>(kCostItem) + keys * kCostWide;
-  if (last) c += tail_keys * (tail > p.tpt ? kCostWide : kCostNarrow<D>);
+  long long c = F * static_cast<long long>(kCostItem) + keys * kCostWide;
+  if (last) c += tail > p.tpt ? kCostItem + tail_keys * kCostWide : kCostItemNarrow + tail_keys * kCostNarrow<D>;
   return c;
 }
 
@@ -244,7 +244,7 @@ template <int D>
 __device__ __forceinline__ void next_piece(const VarlenParams& p, const VlPlan& pl, int cta, VlWalk& w, VlPiece& out) {
   while (w.s < pl.end) {
     const VlGeom g = geom_at(p, w.sq.n, w.sq.nk, w.rt);
-    const long long x0 = w.s + kCostItem;  // where the item's first tile stands
+    const long long x0 = w.s + (g.wide ? kCostItem : kCostItemNarrow);  // where the item's first tile stands
     const int j0 = tile_from<D>(pl.start - x0, g), j1 = tile_from<D>(pl.end - x0, g);
     const int kvh = w.u / p.hchunks, hc = w.u - kvh * p.hchunks;
     out.g = g;
@@ -312,56 +312,11 @@ __device__ __forceinline__ bool vl_tile_is_full(const VarlenParams& p, int qa, i
   return full;
 }
 
-// One key tile of a team's rows: scores from TMEM (colS), the mask, the running
-// maximum and sum of this thread's row, the output row (colO) rescaled where the
-// maximum moved, and the probabilities back over the scores, in two halves.
-// EDGE: visible are the columns [cmin, cmax] and those before csink.
-template <int D, bool EDGE>
-__device__ __forceinline__ void softmax_tile(const VarlenParams& p, uint32_t colS, uint32_t colO, uint32_t bar_lo,
-                                             uint32_t bar_hi, int cmin, int cmax, int csink, bool row_valid,
-                                             float& m_used, float& l_sum) {
-  const float sl2 = p.scale_log2;
-  // On a tile at the mask's edge: the visible keys of this row, a word for
-  // each 32 columns, and whether the warp's rows see none or all of them. What
-  // none sees is not computed; the select stands only where some see and some not.
-  uint32_t vis[kBN / 32], none = 0, some = 0;
-  if (EDGE) {
-#pragma unroll
-    for (int cc = 0; cc < kBN / 32; ++cc) {
-      const int lo = cmin - 32 * cc, hi = cmax - 32 * cc, sk = csink - 32 * cc;
-      const uint32_t from = lo <= 0 ? ~0u : (lo > 31 ? 0u : ~0u << lo);
-      const uint32_t to = hi < 0 ? 0u : (hi > 30 ? ~0u : (2u << hi) - 1u);
-      const uint32_t sink = sk <= 0 ? 0u : (sk > 31 ? ~0u : (1u << sk) - 1u);
-      vis[cc] = row_valid ? (from | sink) & to : 0u;
-      if (!__any_sync(0xffffffffu, vis[cc] != 0u)) none |= 1u << cc;
-      if (!__all_sync(0xffffffffu, vis[cc] == ~0u || !row_valid)) some |= 1u << cc;
-    }
-  }
-  uint32_t raw[kBN];
-#pragma unroll
-  for (int cc = 0; cc < kBN / 32; ++cc)
-    tmem_ld_32x32b_x32(colS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[cc * 32]));
-  tc_wait_ld();
-  float sv[kBN];
-#pragma unroll
-  for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(raw[c]);
-  float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-  for (int cc = 0; cc < kBN / 32; ++cc) {
-    if (EDGE && (none >> cc & 1u)) continue;
-    if (EDGE && (some >> cc & 1u)) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) sv[cc * 32 + e] = vis[cc] >> e & 1u ? sv[cc * 32 + e] : -INFINITY;
-    }
-#pragma unroll
-    for (int c = cc * 32; c < cc * 32 + 32; c += 8) {
-      mx0 = max3f(mx0, sv[c], sv[c + 1]);
-      mx1 = max3f(mx1, sv[c + 2], sv[c + 3]);
-      mx2 = max3f(mx2, sv[c + 4], sv[c + 5]);
-      mx3 = max3f(mx3, sv[c + 6], sv[c + 7]);
-    }
-  }
-  const float m_new = fmaxf(m_used, max3f(mx0, mx1, fmaxf(mx2, mx3)) * sl2);
+// The running maximum of a row takes in a tile's: the sum and, where the maximum
+// moved (lazily, see kVlRescale), the output row in TMEM are rescaled.
+template <int D>
+__device__ __forceinline__ void move_max(float tile_max, uint32_t colO, float& m_used, float& l_sum) {
+  const float m_new = fmaxf(m_used, tile_max);
   bool rescale_o = false;
   float factor = 1.f;
   if (m_new > m_used + kVlRescale) {  // also true for the first visible key (m_used = -inf)
@@ -373,29 +328,58 @@ __device__ __forceinline__ void softmax_tile(const VarlenParams& p, uint32_t col
   }
   // The score barrier was committed after this team's previous P V: O is stable.
   if (__any_sync(0xffffffffu, rescale_o)) rescale_row_t<D>(colO, rescale_o ? factor : 1.f);
-  // a row with nothing visible yet uses m = 0
-  const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
-  float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
+}
+
+// 32 scores to probabilities: p = 2^(s * scale * log2 e - m), their sum into acc.
+__device__ __forceinline__ void exp_32(const float* sv, float sl2, float neg_m, float2 (&acc)[4], uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float2 xv = ffma2(make_float2(sv[2 * e], sv[2 * e + 1]), make_float2(sl2, sl2), make_float2(neg_m, neg_m));
+    float2 pv;
+    pv.x = fast_exp2(xv.x);
+    pv.y = fast_exp2(xv.y);
+    acc[e & 3] = fadd2(acc[e & 3], pv);
+    pk[e] = pack_bf16x2(pv.x, pv.y);
+  }
+}
+__device__ __forceinline__ float sum_8(const float2 (&a)[4]) {
+  return ((a[0].x + a[0].y) + (a[1].x + a[1].y)) + ((a[2].x + a[2].y) + (a[3].x + a[3].y));
+}
+__device__ __forceinline__ float max_32(const float* v, float m) {
+  float mx0 = m, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 32; c += 8) {
+    mx0 = max3f(mx0, v[c], v[c + 1]);
+    mx1 = max3f(mx1, v[c + 2], v[c + 3]);
+    mx2 = max3f(mx2, v[c + 4], v[c + 5]);
+    mx3 = max3f(mx3, v[c + 6], v[c + 7]);
+  }
+  return max3f(mx0, mx1, fmaxf(mx2, mx3));
+}
+
+// One key tile of a team's rows that every row sees: scores from TMEM (colS), the
+// running maximum and sum of this thread's row, and the probabilities back over
+// the scores, in two halves that are announced as they land.
+template <int D>
+__device__ __forceinline__ void softmax_tile(float sl2, uint32_t colS, uint32_t colO, uint32_t bar_lo, uint32_t bar_hi,
+                                             float& m_used, float& l_sum) {
+  uint32_t raw[kBN];
+#pragma unroll
+  for (int cc = 0; cc < kBN / 32; ++cc)
+    tmem_ld_32x32b_x32(colS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[cc * 32]));
+  tc_wait_ld();
+  float sv[kBN];
+#pragma unroll
+  for (int c = 0; c < kBN; ++c) sv[c] = __uint_as_float(raw[c]);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int cc = 0; cc < kBN / 32; ++cc) mx = max_32(&sv[cc * 32], mx);
+  move_max<D>(mx * sl2, colO, m_used, l_sum);
+  float2 acc[4] = {};
 #pragma unroll
   for (int cc = 0; cc < kBN / 32; ++cc) {
     uint32_t pk[16];
-    if (EDGE && (none >> cc & 1u)) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) pk[e] = 0u;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int c = cc * 32 + 2 * e;
-        const float2 xv =
-            ffma2(make_float2(sv[c], sv[c + 1]), make_float2(sl2, sl2), make_float2(neg_m, neg_m));
-        float2 pv;
-        pv.x = fast_exp2(xv.x);
-        pv.y = fast_exp2(xv.y);
-        float2& acc = (e & 3) == 0 ? acc0 : (e & 3) == 1 ? acc1 : (e & 3) == 2 ? acc2 : acc3;
-        acc = fadd2(acc, pv);
-        pk[e] = pack_bf16x2(pv.x, pv.y);
-      }
-    }
+    exp_32(&sv[cc * 32], sl2, -m_used, acc, pk);
     tmem_st_32x32b_x16(colS + cc * 16, pk);  // over score columns already consumed
     if (cc == 1 || cc == 3) {
       tc_wait_st();
@@ -403,7 +387,71 @@ __device__ __forceinline__ void softmax_tile(const VarlenParams& p, uint32_t col
       mbar_arrive(cc == 1 ? bar_lo : bar_hi);
     }
   }
-  l_sum += ((acc0.x + acc0.y) + (acc1.x + acc1.y)) + ((acc2.x + acc2.y) + (acc3.x + acc3.y));
+  l_sum += sum_8(acc);
+}
+
+// The same at the mask's edge: visible to this row are the columns [cmin, cmax]
+// and those before csink. Groups of 32 columns that no row of the warp sees are
+// not computed (with a window most are not), so the groups go one by one, twice:
+// maximum, then exponentials, each from TMEM.
+template <int D>
+__device__ __forceinline__ void softmax_edge_tile(float sl2, uint32_t colS, uint32_t colO, uint32_t bar_lo,
+                                                  uint32_t bar_hi, int cmin, int cmax, int csink, bool row_valid,
+                                                  float& m_used, float& l_sum) {
+  auto visible = [&](int cc) -> uint32_t {
+    const int lo = cmin - 32 * cc, hi = cmax - 32 * cc, sk = csink - 32 * cc;
+    const uint32_t from = lo <= 0 ? ~0u : (lo > 31 ? 0u : ~0u << lo);
+    const uint32_t to = hi < 0 ? 0u : (hi > 30 ? ~0u : (2u << hi) - 1u);
+    const uint32_t sink = sk <= 0 ? 0u : (sk > 31 ? ~0u : (1u << sk) - 1u);
+    return row_valid ? (from | sink) & to : 0u;
+  };
+  // some: not all rows see the whole group (else nothing is left to mask)
+  auto load = [&](int cc, uint32_t vis, bool some, float (&sv)[32]) {
+    uint32_t raw[32];
+    tmem_ld_32x32b_x32(colS + cc * 32, raw);
+    tc_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 32; ++e) sv[e] = __uint_as_float(raw[e]);
+    if (some) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) sv[e] = vis & (1u << e) ? sv[e] : -INFINITY;
+    }
+  };
+  float mx = -INFINITY;
+  unsigned seen = 0, part = 0;
+#pragma unroll 1
+  for (int cc = 0; cc < kBN / 32; ++cc) {
+    const uint32_t vis = visible(cc);
+    if (!__any_sync(0xffffffffu, vis != 0u)) continue;
+    const bool some = !__all_sync(0xffffffffu, vis == ~0u || !row_valid);
+    seen |= 1u << cc;
+    part |= static_cast<unsigned>(some) << cc;
+    float sv[32];
+    load(cc, vis, some, sv);
+    mx = max_32(sv, mx);
+  }
+  move_max<D>(mx * sl2, colO, m_used, l_sum);
+  const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;  // a row with nothing visible yet uses m = 0
+  float2 acc[4] = {};
+#pragma unroll 1
+  for (int cc = 0; cc < kBN / 32; ++cc) {
+    uint32_t pk[16];
+    if (seen >> cc & 1u) {
+      float sv[32];
+      load(cc, visible(cc), part >> cc & 1u, sv);
+      exp_32(sv, sl2, neg_m, acc, pk);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = 0u;
+    }
+    tmem_st_32x32b_x16(colS + cc * 16, pk);  // group cc / 2 of the scores has been read
+    if (cc & 1) {
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(cc == 1 ? bar_lo : bar_hi);
+    }
+  }
+  l_sum += sum_8(acc);
 }
 
 __device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
@@ -866,7 +914,9 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       const bool active = wr >= 0 && wr * 32 < ntok * p.gsz;  // the warp has rows of the item
       const bool row_valid = active && rtok < ntok && rhead < nheads;
       const float sink2 = p.sinks != nullptr && row_valid ? __ldg(p.sinks + head0 + rhead) * kLog2e : -INFINITY;
-      float m_used = -INFINITY;  // max the exponentials are taken against (base 2)
+      // Max the exponentials are taken against (base 2). Rows that are none: +inf, so
+      // that their probabilities are 0 (no output is made of them; zeros cost less power).
+      float m_used = row_valid ? -INFINITY : INFINITY;
       float l_sum = 0.f;         // running sum of 2^(s - m_used)
       for (int j = wide ? 0 : x; j < nt && ok; j += wide ? 1 : 2, ++cnt) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar(kVbSFull + x), cnt & 1, budget, abort_flag));
@@ -878,14 +928,13 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         }
         const int k0 = gm.tile_key(pc.j0 + j);
         tc_fence_after();
-        // A tile inside the mask runs without any of the edge's branches.
         if (vl_tile_is_full(p, qa, qa + ntok - 1, k0, pc.nk))
-          softmax_tile<D, false>(p, colS, colO, bar(kVbPLo + x), bar(kVbPHi + x), 0, 0, 0, true, m_used, l_sum);
+          softmax_tile<D>(p.scale_log2, colS, colO, bar(kVbPLo + x), bar(kVbPHi + x), m_used, l_sum);
         else
-          softmax_tile<D, true>(p, colS, colO, bar(kVbPLo + x), bar(kVbPHi + x),
-                                p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? qa + rtok - k0 - p.window + 1 : 0,
-                                (p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : qa + rtok) - k0, p.n_sink - k0, row_valid,
-                                m_used, l_sum);
+          softmax_edge_tile<D>(p.scale_log2, colS, colO, bar(kVbPLo + x), bar(kVbPHi + x),
+                               p.mask_kind == ATTN_MASK_SLIDING_WINDOW ? qa + rtok - k0 - p.window + 1 : 0,
+                               (p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : qa + rtok) - k0, p.n_sink - k0, row_valid,
+                               m_used, l_sum);
       }
       const bool took_part = wide || nt > x;
       if (ok && took_part)

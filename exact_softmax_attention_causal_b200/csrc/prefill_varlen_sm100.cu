@@ -110,8 +110,9 @@ enum : int {
   kVbQEmpty = 28,
   kVbPiece = 29,      // + entry of the piece ring (4)
   kVbPieceDone = 33,  // + entry
+  kVbPair = 37,       // + pair of warps that join rows (4, and 2 where team 1 is shifted)
 };
-constexpr int kVbTmemSlot = 312, kVbAbort = 316;  // bytes behind the barriers
+constexpr int kVbTmemSlot = 352, kVbAbort = 356;  // bytes behind the barriers
 constexpr int kPieces = 4;                        // pieces worked out ahead
 
 // An item whose first piece is CTA c's last: what the joining grid needs of it.
@@ -375,11 +376,12 @@ __device__ __forceinline__ void softmax_tile(float sl2, uint32_t colS, uint32_t 
 #pragma unroll
   for (int cc = 0; cc < kBN / 32; ++cc) mx = max_32(&sv[cc * 32], mx);
   move_max<D>(mx * sl2, colO, m_used, l_sum);
+  const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;  // scores of -inf alone
   float2 acc[4] = {};
 #pragma unroll
   for (int cc = 0; cc < kBN / 32; ++cc) {
     uint32_t pk[16];
-    exp_32(&sv[cc * 32], sl2, -m_used, acc, pk);
+    exp_32(&sv[cc * 32], sl2, neg_m, acc, pk);
     tmem_st_32x32b_x16(colS + cc * 16, pk);  // over score columns already consumed
     if (cc == 1 || cc == 3) {
       tc_wait_st();
@@ -454,8 +456,6 @@ __device__ __forceinline__ void softmax_edge_tile(float sl2, uint32_t colS, uint
   l_sum += sum_8(acc);
 }
 
-__device__ __forceinline__ void pair_barrier(int id) { asm volatile("bar.sync %0, 64;\n" ::"r"(id) : "memory"); }
-
 template <int D>
 __global__ void __launch_bounds__(kVlThreads, 1)
     prefill_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_qh,
@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       mbar_init(bar(kVbPiece + s), 1);
       mbar_init(bar(kVbPieceDone + s), 11);  // both TMA warps, the MMA thread, 8 softmax warps
     }
+    for (int s = 0; s < 6; ++s) mbar_init(bar(kVbPair + s), 2);
     mbar_init(bar(kVbDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -868,17 +869,19 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       }
       __syncwarp();
       // then the rows of sequences whose lengths do not fit
-      for (int b = cta; b < p.B; b += gridDim.x) {
-        const VlSeq sq = seq_at(p, b);
-        if (!sq.bad) continue;
-        if (lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
-        const int r0 = max(0, sq.row0), r1 = min(p.T, __ldg(p.cu_q + b + 1));
-        for (int r = r0; r < r1; ++r) {
-          __nv_bfloat16* row = p.o + static_cast<size_t>(r) * p.Hq * D;
-          for (int i = lane; i < p.Hq * D / 8; i += 32)
-            reinterpret_cast<uint4*>(row)[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-          if (p.lse != nullptr)
-            for (int i = lane; i < p.Hq; i += 32) p.lse[static_cast<size_t>(r) * p.Hq + i] = NAN;
+      for (int base = cta * 32; base < p.B; base += gridDim.x * 32) {
+        const bool mine = base + lane < p.B && seq_at(p, base + lane).bad;
+        for (unsigned bad = __ballot_sync(0xffffffffu, mine); bad != 0; bad &= bad - 1) {
+          const int b = base + __ffs(bad) - 1;
+          if (lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
+          const int r0 = max(0, __ldg(p.cu_q + b)), r1 = min(p.T, __ldg(p.cu_q + b + 1));
+          for (int r = r0; r < r1; ++r) {
+            __nv_bfloat16* row = p.o + static_cast<size_t>(r) * p.Hq * D;
+            for (int i = lane; i < p.Hq * D / 8; i += 32)
+              reinterpret_cast<uint4*>(row)[i] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+            if (p.lse != nullptr)
+              for (int i = lane; i < p.Hq; i += 32) p.lse[static_cast<size_t>(r) * p.Hq + i] = NAN;
+          }
         }
       }
     }
@@ -892,6 +895,17 @@ __global__ void __launch_bounds__(kVlThreads, 1)
     const uint32_t colO = lane_base + C::col_o(x);
     int cnt = 0, fin = 0, it = 0;  // this team's score tiles, finished outputs; items
     bool ok = true;
+    // Both warps of pair `id` have come here. Bounded like every wait: after an expired
+    // wait elsewhere the other warp may have left.
+    uint32_t pair_par = 0;
+    auto pair_sync = [&](int id) -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kVbPair + id));
+      const bool r =
+          __all_sync(0xffffffffu, mbar_wait_bounded(bar(kVbPair + id), (pair_par >> id) & 1u, budget, abort_flag));
+      pair_par ^= 1u << id;
+      return r;
+    };
     for (; ok; ++it) {
       ok = __all_sync(0xffffffffu, piece_wait(it));
       if (!ok) break;
@@ -957,14 +971,14 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       // ---- the two teams of a narrow item are joined: both know both sums, team 1
       // hands its output over in 32-column pieces through its staging box
       const bool join = !wide && nt > 1;
-      const int other_warp = x == 0 ? warp + 4 + (pc.half ? 2 : 0) : wr;
+      const int other_warp = x == 0 ? warp + 4 + (pc.half ? 2 : 0) : wr, pair = wr + (pc.half ? 4 : 0);
       float f = 1.f;
       if (join) {
         float2* mine = reinterpret_cast<float2*>(smem + C::kStageOff + warp * 4096);
         mine[lane] = make_float2(m_used, ok ? l_sum : NAN);
-        pair_barrier(1 + wr);
+        if (!pair_sync(pair)) ok = false;
         const float2 other = reinterpret_cast<float2*>(smem + C::kStageOff + other_warp * 4096)[lane];
-        pair_barrier(1 + wr);  // read before the boxes are written again
+        if (!pair_sync(pair)) ok = false;  // read before the boxes are written again
         const float m = fmaxf(m_used, other.x);
         f = m_used == -INFINITY ? 0.f : exp2f(m_used - m);
         l_sum = l_sum * f + (other.x == -INFINITY ? 0.f * other.y : other.y * exp2f(other.x - m));
@@ -979,9 +993,10 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           tc_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) box[e * 32 + lane] = f == 0.f ? 0.f : __uint_as_float(ov[e]) * f;
-          pair_barrier(1 + wr);
-          pair_barrier(1 + wr);
+          if (!pair_sync(pair)) ok = false;
+          if (!pair_sync(pair)) ok = false;
         }
+        if (!ok) raise_abort(abort_flag, p.status);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) piece_done(it);
@@ -1021,11 +1036,12 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           tmem_ld_32x32b_x32(colO + hh * 64 + q32 * 32, ov);
           tc_wait_ld();
           if (join) {
-            pair_barrier(1 + wr);
+            if (!pair_sync(pair)) ok = false;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               ov[e] = __float_as_uint((f == 0.f ? 0.f : __uint_as_float(ov[e]) * f) + box[e * 32 + lane]);
-            pair_barrier(1 + wr);
+            if (!pair_sync(pair)) ok = false;
+            if (!ok) norm = NAN;
           }
           if (whole) {
 #pragma unroll
@@ -1073,6 +1089,10 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           }
           __syncwarp();
         }
+      }
+      if (join && !ok) {
+        raise_abort(abort_flag, p.status);
+        if (!whole) p.part_ml[static_cast<size_t>(pc.slot) * kVlRows + x * kBM + r] = make_float2(m_used, NAN);
       }
       // The next item's first P V overwrites O: its P is announced only after
       // these loads completed (tcgen05.wait::ld above, fence before the arrive).

@@ -304,6 +304,55 @@ def test_named_stream_and_workspace_bounds():
         prefill_paged_varlen(*args, b.max_len, workspace=buf[:n - 16])
 
 
+@pytest.mark.parametrize("n,ctx,Hq,Hkv,d", [([300, 200], [2000, 900], 8, 2, 128), ([1, 3, 8], [3000, 700, 5000], 8, 2, 64),
+                                            ([1, 150, 2], [9000, 4000, 300], 16, 2, 128)])
+def test_an_expired_wait_is_reported_and_ends(monkeypatch, n, ctx, Hq, Hkv, d):
+    """A one-cycle budget lets the pipeline's waits give up: the call comes back with the timeout bit, NaN rows where
+    work was left, writes nothing else, and the next call is right. The budget counts from behind the first try, which
+    the hardware may itself hold for longer than a short item's copies take: where the few tiles a multiprocessor has
+    come through on first tries alone, no bit is set and every row has to be right."""
+    b = Batch(n, ctx, Hq, Hkv, d, 16, 21)
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    q, *rest = b.args()
+    q = torch.cat([q, q[:7]])
+    out = torch.full((b.T + 7, Hq, d), 5.0, dtype=BF16, device="cuda")
+    lse = torch.full((b.T + 7, Hq), 5.0, device="cuda")
+    monkeypatch.setenv("ATTN_WAIT_BUDGET_CYCLES", "1")
+    prefill_paged_varlen(q, *rest, b.max_len, out=out, lse=lse, status=status)
+    torch.cuda.synchronize()
+    monkeypatch.delenv("ATTN_WAIT_BUDGET_CYCLES")
+    if int(status.item()) == 0:
+        assert max(ctx) * Hkv <= 10000  # the largest batch has more tiles a multiprocessor than its ring holds
+        b.check(out[:b.T], lse[:b.T])
+    else:
+        assert int(status.item()) == 0x2 and torch.isnan(out[:b.T].float()).any()
+    assert not (out[:b.T] == 5).all(-1).any() and (out[b.T:] == 5).all() and (lse[b.T:] == 5).all()
+    b.run_and_check()
+
+
+def test_scores_without_a_finite_value():
+    """An infinite key element makes whole scores -inf: such keys weigh nothing, the others are as without them."""
+    b = Batch([3, 70], [400, 300], 4, 2, 64, 16, 22)
+    b.q = b.q.abs() + 0.125
+    for k in b.k:
+        k[:256 if len(k) > 300 else 140, :, 0] = -math.inf
+    for s, c in enumerate(b.ctx):
+        t = torch.arange(c)
+        b.k_cache[b.table[s].long()[t // 16], t % 16] = b.k[s]
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    o, lse = b.run(status=status)
+    assert int(status.item()) == 0
+    for s, (n, c) in enumerate(zip(b.n, b.ctx)):
+        gone = 256 if c > 300 else 140
+        cut = Batch.__new__(Batch)
+        cut.__dict__.update(b.__dict__)
+        # the same rows against the keys that are left
+        cut.n, cut.ctx, cut.k, cut.v = [n], [c - gone], [b.k[s][gone:]], [b.v[s][gone:]]
+        cut.q, cut.cu = b.q[int(b.cu[s]):int(b.cu[s + 1])], torch.tensor([0, n])
+        r = slice(int(b.cu[s]), int(b.cu[s + 1]))
+        cut.check(o[r], lse[r])
+
+
 def test_refusals():
     b = Batch([2, 3], [20, 30], 4, 2, 64, 16, 20)
     q, kc, vc, bt, cu, sl = b.args()

@@ -107,10 +107,12 @@ enum : int {
   kVbPHi = 23,     // + team: probabilities of keys 64-127 written
   kVbOFinal = 25,  // + team
   kVbDrain = 27,
+  // + item (mod 2): the V warp may look for an item's phase when the next item's is
+  // over too, and the parity of one barrier's phases would not tell them apart
   kVbQEmpty = 28,
-  kVbPiece = 29,      // + entry of the piece ring (4)
-  kVbPieceDone = 33,  // + entry
-  kVbPair = 37,       // + pair of warps that join rows (4, and 2 where team 1 is shifted)
+  kVbPiece = 30,      // + entry of the piece ring (4)
+  kVbPieceDone = 34,  // + entry
+  kVbPair = 38,       // + pair of warps that join rows (4, and 2 where team 1 is shifted)
 };
 constexpr int kVbTmemSlot = 352, kVbAbort = 356;  // bytes behind the barriers
 constexpr int kPieces = 4;                        // pieces worked out ahead
@@ -485,6 +487,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(bar(kVbQFull), 1);
     mbar_init(bar(kVbQEmpty), 1);
+    mbar_init(bar(kVbQEmpty + 1), 1);
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(kVbKFull + s), 1);
       mbar_init(bar(kVbKEmpty + s), 1);
@@ -657,7 +660,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         // read its Q, and a wide item's Q waits for the slot's last V tile.
         bool armed = true;
         if (lane == 0) {
-          armed = (it == 0) || mbar_wait_bounded(bar(kVbQEmpty), (it - 1) & 1, budget, abort_flag);
+          armed = (it == 0) || mbar_wait_bounded(bar(kVbQEmpty + ((it - 1) & 1)), ((it - 1) >> 1) & 1, budget, abort_flag);
           if (k_warp) {
             if (armed && gm.wide)
               armed = mbar_wait_bounded(bar(kVbVEmpty + C::kStages), vr.phase(C::kStages) ^ 1u, budget, abort_flag);
@@ -815,7 +818,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           issue_s(wide ? 0 : j, 0, g + j);
           if (wide) issue_s(1, 1, g);
           tc_commit_w(bar(kVbKEmpty + (g + j) % C::kStages));
-          if (j == nt - 1) tc_commit_w(bar(kVbQEmpty));
+          if (j == nt - 1) tc_commit_w(bar(kVbQEmpty + (it & 1)));
         }
         for (int j = 0; j < nt && ok; ++j) {
           const int jn = j + ahead;
@@ -837,7 +840,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
               issue_s(x, wide ? t : 0, g + jn);
               if (last_team) {
                 tc_commit_w(bar(kVbKEmpty + (g + jn) % C::kStages));
-                if (jn == nt - 1) tc_commit_w(bar(kVbQEmpty));  // that was the item's last read of Q
+                if (jn == nt - 1) tc_commit_w(bar(kVbQEmpty + (it & 1)));  // that was the item's last read of Q
               }
             }
           }

@@ -520,7 +520,7 @@ def _table_args(seq_lens, second, second_name, block_table, free_blocks, num_fre
 def _int32_outs(given, dev):
     """Outputs [n] int32: those of (tensor or None, name, n) that the caller gave, the others out of one allocation."""
     sizes = [n for t, _, n in given if t is None]
-    fresh = iter(torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes) if sizes else ())
+    fresh = iter(torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes) if sizes else ())
     outs = []
     for t, name, n in given:
         if t is None:

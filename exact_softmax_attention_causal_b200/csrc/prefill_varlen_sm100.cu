@@ -27,13 +27,23 @@
 // has at most two partials, one per end, so the workspace does not depend on
 // the batch.
 //
-// What bounds it: HBM for narrow items (64 KB of K and V a tile at d = 128,
-// 1.45 us of an SM's share of HBM, against 0.55 us of MMAs), the softmax and the
-// tensor cores for wide ones.
+// What bounds it. Narrow items: HBM (64 KB of K and V a tile at d = 128, 1.45 us of
+// an SM's share of HBM, against 0.55 us of MMAs); at d = 64 the chain scores ->
+// softmax -> P V -> scores of the two teams. Wide items: that chain, the softmax's
+// exponentials and the tensor cores in turn, as in the prefill kernel. Short items
+// (a window of 128): the latency of an item's steps, 13,000 cycles for two tiles.
+// Measured: 64 sequences of 1K-32K tokens with 1-8 rows each, 32 / 8 heads, d = 128
+// 640 us (6,610 GB/s, the copy's rate); one of 131,072 tokens 108 us (5,000 GB/s);
+// 4 chunks of 2,048 rows on 16,384 tokens 1,860 us (1,110 TFLOP/s); 4 chunks of
+// 1K-2K rows beside 32 single rows 1,140 us; 48 chunks of up to 512 rows and 16
+// single ones, window 128, 64 / 8 heads, d = 64 222 us.
 //
 // Roles, pipeline and the lazily moved maximum are those of the prefill kernel
-// (prefill_sm100.cu): 8 softmax warps, one TMA warp, one MMA warp; probabilities
-// go to the second product as bf16 (the tensor cores take nothing wider at this
+// (prefill_sm100.cu): 8 softmax warps, an MMA warp, here two TMA warps (K and V),
+// and a warp that works out the items ahead of their use. (An MMA warp for each
+// team was slower: their products wait for one another in the tensor cores' queue,
+// 4,400 cycles a wide tile instead of 3,450.) Probabilities go to the second
+// product as bf16 (the tensor cores take nothing wider at this
 // rate; 2^-9 of each p, averaged over the row), sums and outputs stay in fp32.
 
 #include <cuda.h>
@@ -65,7 +75,8 @@ static_assert(256 * kVlRegsSoftmax + 128 * kVlRegsControl == kVlThreads * 168, "
 constexpr float kVlRescale = 8.0f;  // base 2: the maximum moves only past this (p <= 2^8)
 // What a key costs on the line, and what an item costs besides, in proportion to
 // the cycles measured: a wide tile of 128 keys 3,650 (d = 128) and 3,300 (d = 64),
-// a narrow one COSTN, an item's ends 5,000.
+// a narrow one 2,300 and 1,850 where HBM is shared by all, a wide item's ends 5,000,
+// a narrow one's (its teams' outputs are joined) 9,000.
 constexpr int kCostWide = 20, kCostItem = 28 * kBN, kCostItemNarrow = 48 * kBN;
 template <int D>
 constexpr int kCostNarrow = D == 128 ? 11 : 8;
@@ -618,7 +629,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
     if (warp == kVlTmaWarp || warp == kVlTmaVWarp) {
       // ---------------------------------------------------------- TMA producers: Q and K by one warp, V by the other
       // (a box of a block of 16 tokens takes about as long to issue as to move:
-      // one warp for both kept HBM at 73 % where two reach REACH %).
+      // one warp for both held 64 sequences of 1K-32K tokens at 4,800 GB/s, two reach 6,180).
       // Lane 0 waits on the ring and arms the barriers, lane e copies block e of a
       // key tile, its table entry read one tile ahead. A block that no row of the
       // item sees, that lies past the sequence or whose entry is outside the pool is
@@ -923,8 +934,8 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       const int qa = gm.pos_lo + t0;
       // This thread's row of the item's tile, its token and head. A narrow item of at
       // most 64 rows stands in the lanes 64 and up for team 1: its warps then run on
-      // the SM partitions that team 0's leave idle (warps 0 and 4 share one, and at
-      // 128 exponentials a row it was the limit: SAMEPART cycles a tile at d = 64).
+      // the SM partitions that team 0's leave idle (warps 0 and 4 share one; with both
+      // teams on it a tile at d = 64 took 1,910 cycles, so 1,857).
       const int shift = pc.half && x == 1 ? 2 : 0;  // in warps
       const int wr = (warp & 3) - shift, row = wr * 32 + lane;
       const int rtok = (row * p.row_magic) >> 16, rhead = row - rtok * p.gsz;
@@ -1138,8 +1149,9 @@ __global__ void __launch_bounds__(kVlThreads, 1)
 
 // Joins the pieces of the item that CTA blockIdx.x of the grid above started
 // and did not finish: out = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), in
-// the order of the pieces. A thread takes 4 columns of a row.
-constexpr int kJoinThreads = 256, kJoinParts = 8;
+// the order of the pieces, kJoinBatch of them loaded at a time. A thread takes 4
+// columns of a row.
+constexpr int kJoinThreads = 256, kJoinParts = 8, kJoinBatch = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) prefill_varlen_join_kernel(const VarlenParams p) {
@@ -1156,23 +1168,36 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_varlen_join_kernel(const
     const int tok = (row >> 7) * p.tpt + tk;
     if (tk >= p.tpt || tok >= sp.ntok || hd >= sp.nheads) continue;
     const float sk = p.sinks != nullptr ? __ldg(p.sinks + sp.head0 + hd) * kLog2e : -INFINITY;
-    float m = sk;
-#pragma unroll 4
-    for (int k = 0; k < sp.pieces; ++k) m = fmaxf(m, p.part_ml[static_cast<size_t>(2 * (c + k) + (k == 0)) * kVlRows + row].x);
-    float l = p.sinks != nullptr ? exp2f(sk - m) : 0.f;
+    float m = sk, l = p.sinks != nullptr ? 1.f : 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < sp.pieces; ++k) {
-      const size_t slot = 2 * (c + k) + (k == 0);
-      const float2 ml = p.part_ml[slot * kVlRows + row];
-      const float4 v = p.part_o[(slot * (D / 4) + c4) * kVlRows + row];
-      // a piece in which this row sees nothing has the maximum -inf, the sum 0 and the output 0
-      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - m);
-      l += ml.y * f;
-      acc.x += v.x * f;
-      acc.y += v.y * f;
-      acc.z += v.z * f;
-      acc.w += v.w * f;
+    for (int k0 = 0; k0 < sp.pieces; k0 += kJoinBatch) {  // loads of kJoinBatch pieces in flight
+      float2 ml[kJoinBatch];
+      float4 v[kJoinBatch];
+#pragma unroll
+      for (int j = 0; j < kJoinBatch; ++j) {
+        const int k = min(k0 + j, sp.pieces - 1);
+        const size_t slot = 2 * (c + k) + (k == 0);
+        ml[j] = p.part_ml[slot * kVlRows + row];
+        v[j] = p.part_o[(slot * (D / 4) + c4) * kVlRows + row];
+      }
+      float m_new = m;
+#pragma unroll
+      for (int j = 0; j < kJoinBatch; ++j) m_new = fmaxf(m_new, ml[j].x);
+      // what has seen nothing yet has the maximum -inf, the sum 0 and the output 0
+      const float f0 = m == -INFINITY ? 0.f : exp2f(m - m_new);
+      l *= f0;
+      acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+      m = m_new;
+#pragma unroll
+      for (int j = 0; j < kJoinBatch; ++j) {
+        if (k0 + j >= sp.pieces) break;
+        const float f = ml[j].x == -INFINITY ? 0.f : exp2f(ml[j].x - m);
+        l += ml[j].y * f;
+        acc.x += v[j].x * f;
+        acc.y += v[j].y * f;
+        acc.z += v[j].z * f;
+        acc.w += v[j].w * f;
+      }
     }
     const float inv = 1.f / l;
     const size_t out = static_cast<size_t>(sp.row0 + tok) * p.Hq + sp.head0 + hd;

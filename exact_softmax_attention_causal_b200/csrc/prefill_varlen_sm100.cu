@@ -1027,6 +1027,10 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           m = fmaxf(m_used, sink2);
           ff = exp2f(m_used - m);
           l = l * ff + exp2f(sink2 - m);
+          if (row_valid && !(sink2 < INFINITY)) {  // NaN or +inf
+            l = NAN;
+            if (p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
+          }
         }
         norm = ff / l;
         if (row_valid && p.lse != nullptr)
@@ -1198,6 +1202,10 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_varlen_join_kernel(const
         acc.z += v[j].z * f;
         acc.w += v[j].w * f;
       }
+    }
+    if (p.sinks != nullptr && !(sk < INFINITY)) {  // NaN or +inf
+      l = NAN;
+      if (p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
     }
     const float inv = 1.f / l;
     const size_t out = static_cast<size_t>(sp.row0 + tok) * p.Hq + sp.head0 + hd;

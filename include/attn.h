@@ -411,7 +411,7 @@ ATTN_API size_t attn_prefill_paged_varlen_workspace_bytes(int d);
  *                with a key that some row of the batch's work on them sees
  *   cu_q         [B + 1] int32, row offsets, ascending           read
  *   seq_lens     [B] int32, cached tokens, the new ones included read
- *   sinks        [Hq] fp32 learned sink logits, or NULL          read
+ *   sinks        [Hq] fp32 learned sink logits (-infinity: none for that head), or NULL   read
  *   o            [T, Hq, d] bf16                                 written
  *   lse          [T, Hq] fp32 (natural log, sink included), or NULL   written
  *   n_sink       with a window: the first n_sink positions stay visible
@@ -427,7 +427,8 @@ ATTN_API size_t attn_prefill_paged_varlen_workspace_bytes(int d);
  * Device checks (ATTN_STATUS_BIT_DEVICE_CHECK): a sequence with rows and a
  * length below their number or above max_seq_len, or with offsets out of order
  * or past T, gets NaN rows (those inside the tensor); a table entry outside the
- * pool gives NaN in the rows that need it.
+ * pool gives NaN in the rows that need it, a sink logit of NaN or +infinity in
+ * its head's.
  *
  * Errors (nothing is launched): ATTN_ERR_INVALID_ARG for NULL or misaligned
  * pointers, bad sizes, Hq % Hkv != 0, a table row shorter than max_seq_len, a

@@ -167,6 +167,17 @@ def test_sink_logits_far_from_the_scores():
         b.run_and_check()
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+def test_sink_logits_that_are_none_are_flagged(value):
+    b = Batch([2, 70, 1], [300, 400, 9000], 4, 2, 64, 16, 9, sinks=True)
+    b.sinks[1] = value
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    o, lse = b.run(status=status)
+    assert int(status.item()) == 1
+    assert torch.isnan(o[:, 1].float()).all() and torch.isnan(lse[:, 1]).all()
+    assert torch.isfinite(o[:, [0, 2, 3]].float()).all() and torch.isfinite(lse[:, [0, 2, 3]]).all()
+
+
 def test_blocks_that_no_row_sees_are_not_read():
     """A window's dropped blocks: entries of -1, and blocks full of NaN."""
     b = Batch([3, 100], [1000, 1500], 8, 2, 64, 16, 10)

@@ -34,7 +34,7 @@ def nvcc() -> str:
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     srcs = [os.path.join(HERE, s) for s in SOURCES]
-    deps = srcs + [os.path.join(HERE, h) for h in ("ptx.cuh", "internal.h", "prefill_tiles.cuh")] + [os.path.join(ROOT, "include", "attn.h")]
+    deps = srcs + [os.path.join(HERE, h) for h in ("ptx.cuh", "internal.h")] + [os.path.join(ROOT, "include", "attn.h")]
     if not force and os.path.exists(LIB) and all(os.path.getmtime(LIB) >= os.path.getmtime(d) for d in deps):
         return LIB
     cmd = [nvcc(), "-O3", "-std=c++17", *ARCH, "-lineinfo", "-shared", "-Xcompiler", "-fPIC",

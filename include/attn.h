@@ -21,15 +21,15 @@
  *                        sections 9, 10 and 12).
  *   attn_prefill_paged - the newest Nq positions of each sequence against its
  *                        paged context (prefix / chunked prefill).
+ *   attn_prefill_paged_varlen - the same with each sequence's own number of
+ *                        query rows, packed: prompt chunks, drafted tokens and
+ *                        single decoded tokens in one call.
  *   attn_prefill_backward - dQ, dK, dV of attn_prefill for an output gradient
  *                        dO, recomputing S and P tile by tile from the saved
  *                        LSE ("Inference attention" post, "FlashAttention").
  *   attn_mla_decode_paged - absorbed Multi-head Latent Attention decode over a
  *                        paged latent cache ("Modern Attention Mechanisms",
  *                        section 7; "Module 09", the MLA section).
- *   attn_prefill_paged_varlen - the same with each sequence's own number of
- *                        query rows, packed: prompt chunks, drafted tokens and
- *                        single decoded tokens in one call.
  *   attn_paged_extend, attn_paged_release - block tables, positions and slot
  *                        maps built on the GPU from the requests' lengths.
  *   attn_qk_norm_rope (and _backward, _paged) - query and key norms with the

@@ -15,7 +15,6 @@ is no CPU or PyTorch fallback, and calls raise if the library is not built.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 
 import torch
@@ -370,27 +369,26 @@ def paged_gather(cache, block_table, seq_lens, max_seq_len: int, out=None, statu
     return out
 
 
-def _entry(fn):
-    """Runs fn with the device of its first argument current and, when the
+def _here(first, stream) -> bool:
+    """Whether a call can run as it stands: no stream named and the device of its first argument current."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("the inputs must be CUDA tensors")
+    return stream is None and first.get_device() == torch._C._cuda_getDevice()
+
+
+def _elsewhere(fn, first, args: dict):
+    """fn again with the device of its first argument current and, when the
     caller names a stream, with that stream current: outputs and workspaces
     then come from that stream's memory, so nothing else can still be using
     them when the kernels run."""
-
-    @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("the inputs must be CUDA tensors")
-        if stream is not None:
-            if stream.device != first.device:
-                raise ValueError(f"stream is on {stream.device}, the inputs on {first.device}")
-            with torch.cuda.stream(stream):
-                return fn(first, *args, **kw)
-        if first.get_device() != torch._C._cuda_getDevice():
-            with torch.cuda.device(first.device):
-                return fn(first, *args, **kw)
-        return fn(first, *args, **kw)
-
-    return call
+    stream = args.pop("stream")
+    if stream is None:
+        with torch.cuda.device(first.device):
+            return fn(**args)
+    if stream.device != first.device:
+        raise ValueError(f"stream is on {stream.device}, the inputs on {first.device}")
+    with torch.cuda.stream(stream):
+        return fn(**args)
 
 
 def _need_on(t, name: str, dtype, shape, dev, strided: bool = False) -> None:
@@ -452,10 +450,9 @@ def prefill_paged_varlen_workspace_bytes(d: int) -> int:
     return n
 
 
-@_entry
 def prefill_paged_varlen(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_seq_len: int, mask: str = "causal",
                          window: int = 0, n_sink: int = 0, sinks=None, scale: float | None = None, out=None, lse=None,
-                         workspace=None, status=None, return_lse: bool = True):
+                         workspace=None, status=None, return_lse: bool = True, stream=None):
     """prefill_paged() with each sequence's own number of query rows, packed;
     returns (O [T, Hq, d], LSE [T, Hq]).
 
@@ -464,9 +461,10 @@ def prefill_paged_varlen(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_s
     [cu_q[b], cu_q[b + 1]), its newest positions; seq_lens [B] int32 counts its
     cached tokens, the new ones included. window, n_sink and sinks as in
     decode_paged_window(), with mask="window". Rows outside [cu_q[0], cu_q[B])
-    of a given out and lse stay as they were (else they are undefined). Keyword
-    stream: the CUDA stream (default: the current one).
+    of a given out and lse stay as they were (else they are undefined).
     """
+    if not _here(q, stream):
+        return _elsewhere(prefill_paged_varlen, q, locals())
     _need_dims(q, "q", 3, "[T, Hq, d]")
     _need_dims(k_cache, "k_cache", 4, "[num_blocks, block_size, Hkv, d]")
     _need_dims(block_table, "block_table", 2, "[B, max_blocks]")
@@ -531,10 +529,9 @@ def _int32_outs(given, dev):
     return outs
 
 
-@_entry
 def paged_extend(seq_lens, new_lens, block_table, free_blocks, num_free, block_size: int, num_blocks: int,
                  max_tokens: int, seq_lens_out=None, num_free_out=None, cu_q=None, positions=None, slots=None,
-                 status=None):
+                 status=None, stream=None):
     """The block table, positions and slot map of one serving step, from the
     requests' lengths; returns (seq_lens_out, num_free_out, cu_q, positions,
     slots) and writes the new entries of block_table.
@@ -545,8 +542,10 @@ def paged_extend(seq_lens, new_lens, block_table, free_blocks, num_free, block_s
     cu_q [B + 1]: sequence b's new tokens are rows [cu_q[b], cu_q[b + 1]).
     seq_lens_out and num_free_out may be seq_lens and num_free themselves. A
     sequence that cannot be served gets the length -1 - seq_lens[b] (negative)
-    and slots of -1, and sets the status bit. Keyword stream: the CUDA stream (default: the current one).
+    and slots of -1, and sets the status bit.
     """
+    if not _here(seq_lens, stream):
+        return _elsewhere(paged_extend, seq_lens, locals())
     dev, B = _table_args(seq_lens, new_lens, "new_lens", block_table, free_blocks, num_free, status)
     n = max(0, int(max_tokens))
     positions, slots, cu_q, seq_lens_out, num_free_out = _int32_outs(
@@ -561,12 +560,13 @@ def paged_extend(seq_lens, new_lens, block_table, free_blocks, num_free, block_s
     return seq_lens_out, num_free_out, cu_q, positions, slots
 
 
-@_entry
 def paged_release(seq_lens, finished, block_table, free_blocks, num_free, block_size: int, num_blocks: int,
-                  seq_lens_out=None, num_free_out=None, status=None):
+                  seq_lens_out=None, num_free_out=None, status=None, stream=None):
     """Puts the blocks of the sequences with finished[b] != 0 (int32) back on
     the free list; returns (seq_lens_out, num_free_out), the finished lengths 0.
     A length -1 - L that paged_extend left counts as L. free_blocks is written from num_free on; in place as paged_extend."""
+    if not _here(seq_lens, stream):
+        return _elsewhere(paged_release, seq_lens, locals())
     dev, B = _table_args(seq_lens, finished, "finished", block_table, free_blocks, num_free, status)
     seq_lens_out, num_free_out = _int32_outs(((seq_lens_out, "seq_lens_out", B), (num_free_out, "num_free_out", 1)), dev)
     rc = _lib.lib().attn_paged_release(seq_lens.data_ptr(), finished.data_ptr(), block_table.data_ptr(),
@@ -613,9 +613,8 @@ def _angles(q_weight, k_weight, cos, sin, positions, pos_shape, d, dev):
     return w_bf16, 2 * cos.shape[1], cos.shape[0]
 
 
-@_entry
 def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: float = 1e-6, interleaved: bool = False,
-                 q_out=None, k_out=None, v_out=None, status=None):
+                 q_out=None, k_out=None, v_out=None, status=None, stream=None):
     """RMS norm of each query and key head and the position rotation in one
     pass, into the layout of prefill(); returns (q, k, v) as [B, H, N, d].
 
@@ -624,8 +623,10 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: flo
     [d] fp32 or bf16, both None for no norm; cos, sin [max_pos, rotary_dim / 2]
     fp32; positions [B, N] int32 (default 0 .. N - 1). The first rotary_dim
     elements turn in pairs (f, f + rotary_dim / 2), or (2 f, 2 f + 1) when
-    interleaved. Keyword stream as in paged_extend.
+    interleaved.
     """
+    if not _here(q, stream):
+        return _elsewhere(qk_norm_rope, q, locals())
     _need_dims(q, "q", 4, "[B, N, Hq, d]")
     _need_dims(k, "k", 4, "[B, N, Hkv, d]")
     dev, (B, N, Hq, d), Hkv = q.device, q.shape, k.shape[2]
@@ -647,13 +648,14 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: flo
     return q_out, k_out, v_out
 
 
-@_entry
 def qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, slots, k_cache, v_cache, eps: float = 1e-6,
-                       interleaved: bool = False, q_out=None, status=None):
+                       interleaved: bool = False, q_out=None, status=None, stream=None):
     """The serving form of qk_norm_rope: packed tokens q [T, Hq, d], k and v
     [T, Hkv, d]; returns q [T, Hq, d] and writes the keys and values into the
     caches [num_blocks, block_size, Hkv, d] at slots [T] (int32, -1: nowhere;
     no slot twice). positions and slots are paged_extend's."""
+    if not _here(q, stream):
+        return _elsewhere(qk_norm_rope_paged, q, locals())
     _need_dims(q, "q", 3, "[T, Hq, d]")
     _need_dims(k, "k", 3, "[T, Hkv, d]")
     dev, (T, Hq, d), Hkv = q.device, q.shape, k.shape[1]
@@ -690,9 +692,8 @@ def qk_norm_rope_backward_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, d: 
     return n
 
 
-@_entry
 def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, positions=None, eps: float = 1e-6,
-                          interleaved: bool = False, dq=None, dk=None, dv=None, workspace=None, status=None):
+                          interleaved: bool = False, dq=None, dk=None, dv=None, workspace=None, status=None, stream=None):
     """Gradients of qk_norm_rope() from those of its outputs, d_q [B, Hq, N, d],
     d_k and d_v [B, Hkv, N, d] (what prefill_backward returns): (dq, dk, dv,
     dq_weight, dk_weight), the weights' in fp32, or None without weights.
@@ -701,6 +702,8 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, pos
     [B, N, Hq + 2 Hkv, d] gradient unless given (any strides with contiguous
     head rows). q, k: the forward's inputs.
     """
+    if not _here(q, stream):
+        return _elsewhere(qk_norm_rope_backward, q, locals())
     _need_dims(q, "q", 4, "[B, N, Hq, d]")
     _need_dims(k, "k", 4, "[B, N, Hkv, d]")
     dev, (B, N, Hq, d), Hkv, bf16 = q.device, q.shape, k.shape[2], torch.bfloat16

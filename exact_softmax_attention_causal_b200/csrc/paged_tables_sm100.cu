@@ -294,7 +294,8 @@ __global__ void __launch_bounds__(kTableThreads, 1) paged_table_kernel(const Tab
 template <bool RELEASE>
 int launch_table(const TableParams& p, long long work, cudaStream_t stream) {
   const int smem = 3 * p.B * static_cast<int>(sizeof(int32_t));
-  if (cudaFuncSetAttribute(paged_table_kernel<RELEASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (smem > 48 * 1024 - 1024 &&  // more than a kernel may have unasked
+      cudaFuncSetAttribute(paged_table_kernel<RELEASE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            3 * kMaxTableSeqs * static_cast<int>(sizeof(int32_t))) != cudaSuccess)
     return ATTN_ERR_CUDA;
   const unsigned ctas = work > kSmallWork ? kTableCluster : 1;

@@ -496,7 +496,8 @@ def prefill_paged_varlen(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_s
                                               _addr(sinks), out.data_ptr(), _addr(lse), B, T, Hq, Hkv, d, num_blocks,
                                               block_size, block_table.shape[1], int(max_seq_len), MASKS[mask],
                                               int(window), int(n_sink), float(scale), workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size(), _addr(status), _current(dev))
+                                              workspace.numel() * workspace.element_size(), _addr(status),
+                                              _current(dev))
     _lib.check(rc, "attn_prefill_paged_varlen")
     return out, lse
 
@@ -564,11 +565,13 @@ def paged_release(seq_lens, finished, block_table, free_blocks, num_free, block_
                   seq_lens_out=None, num_free_out=None, status=None, stream=None):
     """Puts the blocks of the sequences with finished[b] != 0 (int32) back on
     the free list; returns (seq_lens_out, num_free_out), the finished lengths 0.
-    A length -1 - L that paged_extend left counts as L. free_blocks is written from num_free on; in place as paged_extend."""
+    A length -1 - L that paged_extend left counts as L. free_blocks is written
+    from num_free on; in place as paged_extend."""
     if not _here(seq_lens, stream):
         return _elsewhere(paged_release, seq_lens, locals())
     dev, B = _table_args(seq_lens, finished, "finished", block_table, free_blocks, num_free, status)
-    seq_lens_out, num_free_out = _int32_outs(((seq_lens_out, "seq_lens_out", B), (num_free_out, "num_free_out", 1)), dev)
+    seq_lens_out, num_free_out = _int32_outs(((seq_lens_out, "seq_lens_out", B), (num_free_out, "num_free_out", 1)),
+                                             dev)
     rc = _lib.lib().attn_paged_release(seq_lens.data_ptr(), finished.data_ptr(), block_table.data_ptr(),
                                        free_blocks.data_ptr(), num_free.data_ptr(), seq_lens_out.data_ptr(),
                                        num_free_out.data_ptr(), B, int(num_blocks), int(block_size),
@@ -693,7 +696,8 @@ def qk_norm_rope_backward_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, d: 
 
 
 def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, positions=None, eps: float = 1e-6,
-                          interleaved: bool = False, dq=None, dk=None, dv=None, workspace=None, status=None, stream=None):
+                          interleaved: bool = False, dq=None, dk=None, dv=None, workspace=None, status=None,
+                          stream=None):
     """Gradients of qk_norm_rope() from those of its outputs, d_q [B, Hq, N, d],
     d_k and d_v [B, Hkv, N, d] (what prefill_backward returns): (dq, dk, dv,
     dq_weight, dk_weight), the weights' in fp32, or None without weights.

@@ -493,6 +493,8 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
   }
 }
 
+constexpr int kRowsAhead = 10;  // 296 CTAs' rows in one turn
+
 // dw = sum over the CTAs' partial rows (q's, then k's): a CTA takes 32 columns of
 // one of the two, its 32 warps every 32nd row each, then one warp adds the 32 sums.
 template <int D>
@@ -504,7 +506,14 @@ __global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* part, i
   const int col = (blockIdx.x - (is_k ? D / 32 : 0)) * 32 + lane;
   const float* from = part + (is_k ? static_cast<long long>(rows) * D : 0);
   float v = 0.f;
-  for (int r = warp; r < rows; r += 32) v += from[static_cast<long long>(r) * D + col];
+  for (int r0 = warp; r0 < rows; r0 += 32 * kRowsAhead) {  // kRowsAhead rows in flight, summed in order
+    float t[kRowsAhead];
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k)
+      t[k] = r0 + 32 * k < rows ? from[static_cast<long long>(r0 + 32 * k) * D + col] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k) v += t[k];
+  }
   s[warp][lane] = v;
   __syncthreads();
   if (warp == 0) {

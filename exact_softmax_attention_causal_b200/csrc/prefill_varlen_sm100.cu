@@ -616,12 +616,13 @@ __global__ void __launch_bounds__(kVlThreads, 1)
     }
     for (int s = 0; s < kPieces; ++s) {
       mbar_init(bar(kVbPiece + s), 1);
-      mbar_init(bar(kVbPieceDone + s), 11);  // both TMA warps, the MMA thread, 8 softmax warps
+      mbar_init(bar(kVbPieceDone + s), 11);  // both TMA warps, the MMA warp, 8 softmax warps
     }
     for (int s = 0; s < 6; ++s) mbar_init(bar(kVbPair + s), 2);
     mbar_init(bar(kVbDrain), 1);
     *abort_flag = 0;
     fence_mbar_init();
+    p.splits[cta].pieces = 0;
   }
   for (int i = threadIdx.x; i < C::kTile / 16; i += kVlThreads)
     reinterpret_cast<uint4*>(smem + C::kQOff)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -772,7 +773,8 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         // read its Q, and a wide item's Q waits for the slot's last V tile.
         bool armed = true;
         if (lane == 0) {
-          armed = (it == 0) || mbar_wait_bounded(bar(kVbQEmpty + ((it - 1) & 1)), ((it - 1) >> 1) & 1, budget, abort_flag);
+          armed = (it == 0) ||
+                  mbar_wait_bounded(bar(kVbQEmpty + ((it - 1) & 1)), ((it - 1) >> 1) & 1, budget, abort_flag);
           if (k_warp) {
             if (armed && gm.wide)
               armed = mbar_wait_bounded(bar(kVbVEmpty + C::kStages), vr.phase(C::kStages) ^ 1u, budget, abort_flag);
@@ -796,8 +798,8 @@ __global__ void __launch_bounds__(kVlThreads, 1)
           __syncwarp();
           for (int t = lane; t < 2 * C::kHalves * gm.ntok; t += 32) {
             const int tk = t / (2 * C::kHalves), x = t & 1, hh = (t >> 1) & (C::kHalves - 1);
-            tma_load_3d(sbase + C::kQOff + x * 64 * 128 + hh * C::kHalf + tk * p.gsz * 128, &tm_qh, bar(kVbQFull), hh * 64,
-                        pc.head0, pc.row0 + tk);
+            tma_load_3d(sbase + C::kQOff + x * 64 * 128 + hh * C::kHalf + tk * p.gsz * 128, &tm_qh, bar(kVbQFull),
+                        hh * 64, pc.head0, pc.row0 + tk);
           }
         }
         vr.enter(gm.wide);
@@ -961,7 +963,7 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       }
       if (!ok && lane == 0) raise_abort(abort_flag, p.status);
       __syncwarp();
-      // Drain: every MMA this thread issued has completed before TMEM is freed.
+      // Drain: every MMA this warp issued has completed before TMEM is freed.
       tc_commit_w(bar(kVbDrain));
       volatile int never = 0;
       mbar_wait_bounded(bar(kVbDrain), 0, kDrainBudgetCycles, &never);
@@ -969,7 +971,6 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       // ---------------------------------------------------------- the pieces of the stretch, a few ahead of their use
       if (lane == 0) {
         VlWalk w = first_walk();
-        p.splits[cta].pieces = 0;
         for (int it = 0;; ++it) {
           const int e = it % kPieces;
           if (it >= kPieces && !mbar_wait_bounded(bar(kVbPieceDone + e), (it / kPieces - 1) & 1, budget, abort_flag))

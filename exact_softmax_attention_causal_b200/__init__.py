@@ -15,6 +15,7 @@ is no CPU or PyTorch fallback, and calls raise if the library is not built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -519,7 +520,7 @@ def _table_args(seq_lens, second, second_name, block_table, free_blocks, num_fre
 def _int32_outs(given, dev):
     """Outputs [n] int32: those of (tensor or None, name, n) that the caller gave, the others out of one allocation."""
     sizes = [n for t, _, n in given if t is None]
-    fresh = iter(torch.empty(sum(sizes), dtype=torch.int32, device=dev).split_with_sizes(sizes) if sizes else ())
+    fresh = iter(torch.empty(sum(sizes), dtype=torch.int32, device=dev).unsafe_split_with_sizes(sizes) if sizes else ())
     outs = []
     for t, name, n in given:
         if t is None:
@@ -580,7 +581,10 @@ def paged_release(seq_lens, finished, block_table, free_blocks, num_free, block_
     return seq_lens_out, num_free_out
 
 
-_STRIDES6, _STRIDES9 = ctypes.c_int64 * 6, ctypes.c_int64 * 9
+@functools.lru_cache(maxsize=256)
+def _strides(*values):
+    """The host array of element strides that the library reads (made once for each set of values)."""
+    return (ctypes.c_int64 * len(values))(*values)
 
 
 def _need_heads(t, name: str, shape, dev) -> None:
@@ -642,7 +646,7 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: flo
     k_out = _out_on(k_out, "k_out", torch.bfloat16, (B, Hkv, N, d), dev)
     v_out = _out_on(v_out, "v_out", torch.bfloat16, (B, Hkv, N, d), dev)
     rc = _lib.lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                      _STRIDES9(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
+                                      _strides(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
                                       _addr(q_weight), _addr(k_weight), w_bf16, cos.data_ptr(), sin.data_ptr(),
                                       _addr(positions), q_out.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, N,
                                       Hq, Hkv, d, rd, max_pos, float(eps), int(interleaved), _addr(status),
@@ -678,7 +682,7 @@ def qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
     if T == 0:
         return q_out
     rc = _lib.lib().attn_qk_norm_rope_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                            _STRIDES6(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2]),
+                                            _strides(*q.stride()[:2], *k.stride()[:2], *v.stride()[:2]),
                                             _addr(q_weight), _addr(k_weight), w_bf16, cos.data_ptr(), sin.data_ptr(),
                                             positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(),
                                             k_cache.data_ptr(), v_cache.data_ptr(), T, Hq, Hkv, d, num_blocks,
@@ -735,9 +739,9 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, pos
                                     device=dev)
     _need_workspace(workspace, dev)
     rc = _lib.lib().attn_qk_norm_rope_backward(
-        q.data_ptr(), k.data_ptr(), _STRIDES6(*q.stride()[:3], *k.stride()[:3]), _addr(q_weight), _addr(k_weight),
+        q.data_ptr(), k.data_ptr(), _strides(*q.stride()[:3], *k.stride()[:3]), _addr(q_weight), _addr(k_weight),
         w_bf16, cos.data_ptr(), sin.data_ptr(), _addr(positions), d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(),
-        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _STRIDES9(*dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _strides(*dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]),
         _addr(dwq), _addr(dwk), B, N, Hq, Hkv, d, rd, max_pos, float(eps), int(interleaved), _addr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _addr(status), _current(dev))
     _lib.check(rc, "attn_qk_norm_rope_backward")

@@ -299,6 +299,10 @@ int launch_table(const TableParams& p, long long work, cudaStream_t stream) {
                            3 * kMaxTableSeqs * static_cast<int>(sizeof(int32_t))) != cudaSuccess)
     return ATTN_ERR_CUDA;
   const unsigned ctas = work > kSmallWork ? kTableCluster : 1;
+  if (ctas == 1) {  // a cluster of its own, and a cheaper launch
+    paged_table_kernel<RELEASE><<<1, kTableThreads, smem, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kTableThreads);

@@ -140,8 +140,7 @@ int attn_prefill_paged_varlen(const void* q, const void* k_cache, const void* v_
   if (mask_kind != ATTN_MASK_FULL && mask_kind != ATTN_MASK_CAUSAL && mask_kind != ATTN_MASK_SLIDING_WINDOW)
     return ATTN_ERR_INVALID_ARG;
   if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window < 1) return ATTN_ERR_INVALID_ARG;
-  if (n_sink < 0 || n_sink > max_seq_len || (n_sink > 0 && mask_kind != ATTN_MASK_SLIDING_WINDOW))
-    return ATTN_ERR_INVALID_ARG;
+  if (n_sink < 0 || (n_sink > 0 && mask_kind != ATTN_MASK_SLIDING_WINDOW)) return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
   if (!aligned4(block_table) || !aligned4(cu_q) || !aligned4(seq_lens) || !aligned4(sinks) || !aligned4(lse))
@@ -151,6 +150,7 @@ int attn_prefill_paged_varlen(const void* q, const void* k_cache, const void* v_
   // row indices are int32; positions leave room for a window's and a tile's width
   if (static_cast<long long>(T) * Hq > (1LL << 31) - 1 || max_seq_len > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
   if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window >= max_seq_len) mask_kind = ATTN_MASK_CAUSAL, n_sink = 0;
+  if (n_sink > max_seq_len) n_sink = max_seq_len;
   int sms = 0;
   if (current_sm_count(&sms) != ATTN_OK) return ATTN_ERR_CUDA;
   if (!workspace || !aligned16(workspace) || workspace_bytes < varlen_workspace_bytes(d, sms))

@@ -414,7 +414,8 @@ ATTN_API size_t attn_prefill_paged_varlen_workspace_bytes(int d);
  *   sinks        [Hq] fp32 learned sink logits (-infinity: none for that head), or NULL   read
  *   o            [T, Hq, d] bf16                                 written
  *   lse          [T, Hq] fp32 (natural log, sink included), or NULL   written
- *   n_sink       with a window: the first n_sink positions stay visible
+ *   n_sink       with a window: the first n_sink positions stay visible (all of a shorter
+ *                sequence's)
  *   workspace    caller-owned, 16-byte aligned; contents before and after do not matter;
  *                one call at a time
  * Rows of o and lse outside [cu_q[0], cu_q[B]) are left as they were, so a
@@ -432,7 +433,7 @@ ATTN_API size_t attn_prefill_paged_varlen_workspace_bytes(int d);
  *
  * Errors (nothing is launched): ATTN_ERR_INVALID_ARG for NULL or misaligned
  * pointers, bad sizes, Hq % Hkv != 0, a table row shorter than max_seq_len, a
- * bad mask, window or scale, n_sink without a window or above max_seq_len;
+ * bad mask, window or scale, a negative n_sink or one without a window;
  * ATTN_ERR_UNSUPPORTED for d other than 64 or 128, block_size other than 16,
  * 32, 64 or 128, T * Hq of 2^31 or more or max_seq_len above 2^30;
  * ATTN_ERR_WORKSPACE; ATTN_ERR_CUDA when a launch fails.

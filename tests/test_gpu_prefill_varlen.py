@@ -178,6 +178,11 @@ def test_sink_logits_that_are_none_are_flagged(value):
     assert torch.isfinite(o[:, [0, 2, 3]].float()).all() and torch.isfinite(lse[:, [0, 2, 3]]).all()
 
 
+@pytest.mark.parametrize("n_sink", [30, 39, 40, 41, 1000])
+def test_more_sink_positions_than_a_sequence_has(n_sink):
+    Batch([3, 40, 1, 7], [40, 40, 5, 33], 4, 2, 64, 16, 23).run_and_check(mask="window", window=6, n_sink=n_sink)
+
+
 def test_blocks_that_no_row_sees_are_not_read():
     """A window's dropped blocks: entries of -1, and blocks full of NaN."""
     b = Batch([3, 100], [1000, 1500], 8, 2, 64, 16, 10)

@@ -127,7 +127,7 @@ def _varlen(**kw):
     (dict(sinks=ODD), INVALID), (dict(lse=ODD), INVALID), (dict(B=0), INVALID), (dict(T=0), INVALID), (dict(nb=0), INVALID),
     (dict(Hq=6, Hkv=4), INVALID), (dict(mb=7), INVALID), (dict(msl=0), INVALID), (dict(mask=7), INVALID),
     (dict(mask=2, window=0), INVALID), (dict(n_sink=1), INVALID), (dict(mask=2, window=4, n_sink=-1), INVALID),
-    (dict(mask=2, window=4, n_sink=129), INVALID), (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(scale=0.0), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(d=96), UNSUPPORTED), (dict(bs=8, mb=16), UNSUPPORTED), (dict(bs=48, mb=3), UNSUPPORTED),
     (dict(T=1 << 28), UNSUPPORTED), (dict(mb=1 << 27, msl=(1 << 30) + 1), UNSUPPORTED),
 ])

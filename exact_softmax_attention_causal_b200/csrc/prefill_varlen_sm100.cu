@@ -175,10 +175,12 @@ constexpr uint32_t kVlRegsControl = 56;
 static_assert(256 * kVlRegsSoftmax + 128 * kVlRegsControl == kVlThreads * 168, "register split");
 constexpr float kVlRescale = 8.0f;  // base 2: the maximum moves only past this (p <= 2^8)
 // What a key costs on the line, and what an item costs besides, in proportion to
-// the cycles measured: a wide tile of 128 keys 3,650 (d = 128) and 3,300 (d = 64),
-// a narrow one 2,300 and 1,850 where HBM is shared by all, a wide item's ends 5,000,
-// a narrow one's (its teams' outputs are joined) 9,000.
-constexpr int kCostWide = 20, kCostItem = 28 * kBN, kCostItemNarrow = 48 * kBN;
+// the cycles measured (a fit over the SMs of batches of each kind): a wide tile of
+// 128 keys 3,400, a narrow one 1,900 (d = 128) and 1,400 (d = 64) beside wide ones,
+// an item's ends 8,000-13,000. (With 4,800 and 8,200 for a wide and a narrow item's
+// ends the busiest SM of 64 short chunks and 64 short decodes had 25 % more than the
+// mean: 309 us, so 293.)
+constexpr int kCostWide = 20, kCostItem = 60 * kBN, kCostItemNarrow = 74 * kBN;
 template <int D>
 constexpr int kCostNarrow = D == 128 ? 11 : 8;
 // A CTA's stretch holds a tile at least (a piece of every item it passes through).

@@ -29,7 +29,7 @@
 // heads, d = 128 (forward 405 MB, backward 573 MB): one group per 4 heads of a
 // token, groups on a token's heads 113 and 168 us; groups on consecutive tokens
 // 80 and 127; all heads of a token in turn 71 and 120; the steps prefetched 66
-// (93 % of HBM) and 107 (82 %; its two sums a row and three tensors leave 16
+// (93 % of HBM) and 105 (83 %; its two sums a row and three tensors leave 16
 // warps an SM, so latency is not hidden to the end).
 //
 // All arithmetic is in 32 bits; the result is rounded to bf16 once. The weight

@@ -33,10 +33,10 @@
 // exponentials and the tensor cores in turn, as in the prefill kernel. Short items
 // (a window of 128): the latency of an item's steps, 13,000 cycles for two tiles.
 // Measured: 64 sequences of 1K-32K tokens with 1-8 rows each, 32 / 8 heads, d = 128
-// 640 us (6,610 GB/s, the copy's rate); one of 131,072 tokens 108 us (5,000 GB/s);
+// 640 us (6,610 GB/s, the copy's rate); one of 131,072 tokens 105 us (5,100 GB/s);
 // 4 chunks of 2,048 rows on 16,384 tokens 1,860 us (1,110 TFLOP/s); 4 chunks of
 // 1K-2K rows beside 32 single rows 1,140 us; 48 chunks of up to 512 rows and 16
-// single ones, window 128, 64 / 8 heads, d = 64 222 us.
+// single ones, window 128, 64 / 8 heads, d = 64 214 us.
 //
 // Roles, pipeline and the lazily moved maximum are those of the prefill kernel
 // (prefill_sm100.cu): 8 softmax warps, an MMA warp, here two TMA warps (K and V),

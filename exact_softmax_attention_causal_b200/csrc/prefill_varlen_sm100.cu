@@ -1038,8 +1038,9 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       const int qa = gm.pos_lo + t0;
       // This thread's row of the item's tile, its token and head. A narrow item of at
       // most 64 rows stands in the lanes 64 and up for team 1: its warps then run on
-      // the SM partitions that team 0's leave idle (warps 0 and 4 share one; with both
-      // teams on it a tile at d = 64 took 1,910 cycles, so 1,857).
+      // the SM partitions that team 0's leave idle (warps 0 and 4 share one). Sustained,
+      // 4 chunks beside 32 single rows take 1,382 us so and 1,397 with both teams on
+      // the same lanes; batches of narrow items alone the same either way.
       const int shift = pc.half && x == 1 ? 2 : 0;  // in warps
       const int wr = (warp & 3) - shift, row = wr * 32 + lane;
       const int rtok = (row * p.row_magic) >> 16, rhead = row - rtok * p.gsz;

@@ -305,6 +305,39 @@ def test_capture_streams_and_guards():
         qk_norm_rope_backward(q, k, wq, wk, cos, sin, *dz, workspace=buf[:n - 16])
 
 
+def test_offsets_past_32_bits():
+    """Tensors and a pool of more than 2^31 elements: their last rows."""
+    N, Hq, Hkv, d, bs = 140_000, 120, 4, 128, 16
+    qkv = torch.empty((1, N, Hq + 2 * Hkv, d), dtype=BF16, device="cuda")
+    assert qkv.numel() > 2 ** 31 and N * Hq * d > 2 ** 31
+    small = _case(1, 8, Hq, Hkv, d)
+    qkv[:, N - 8:] = torch.cat([_cuda(t) for t in small[:3]], 2)
+    q, k, v = qkv[:, :, :Hq], qkv[:, :, Hq:Hq + Hkv], qkv[:, :, Hq + Hkv:]
+    wq, wk = _cuda(small[3]), _cuda(small[4])
+    cos, sin = [t.cuda() for t in _angles64(N, d)]
+    pos = torch.arange(N - 8, N, dtype=torch.int32, device="cuda")
+    want = qk_norm_rope(q[:, N - 8:].contiguous(), k[:, N - 8:], v[:, N - 8:], wq, wk, cos, sin, positions=pos[None])
+    got = qk_norm_rope(q, k, v, wq, wk, cos, sin)
+    assert all(torch.equal(a, b[:, :, N - 8:]) for a, b in zip(want, got))
+    dz = [torch.empty_like(t) for t in got]
+    for t in dz:
+        t[:, :, N - 8:] = torch.randn(t[:, :, N - 8:].shape, device="cuda").to(BF16)
+    del got
+    # without weights: a weight's gradient would sum the rows nobody filled
+    wantg = qk_norm_rope_backward(q[:, N - 8:], k[:, N - 8:], None, None, cos, sin, *[t[:, :, N - 8:].contiguous() for t in dz],
+                                  positions=pos[None])
+    gotg = qk_norm_rope_backward(q, k, None, None, cos, sin, *dz)
+    assert all(torch.equal(a, b[:, N - 8:]) for a, b in zip(wantg[:3], gotg[:3]))
+    del gotg, dz
+    nb = 270_000
+    kc, vc = (torch.zeros((nb, bs, Hkv, d), dtype=BF16, device="cuda") for _ in range(2))
+    assert kc.numel() > 2 ** 31
+    slots = torch.arange(nb * bs - 8, nb * bs, dtype=torch.int32, device="cuda")
+    qk_norm_rope_paged(q[0, N - 8:], k[0, N - 8:], v[0, N - 8:], wq, wk, cos, sin, pos, slots, kc, vc)
+    assert torch.equal(kc.view(-1, Hkv, d)[-8:], want[1][0].transpose(0, 1)) and torch.equal(vc.view(-1, Hkv, d)[-8:], v[0, N - 8:])
+    assert not kc.view(-1, Hkv, d)[:8].any() and not kc.view(-1, Hkv, d)[-9].any()
+
+
 def test_an_empty_step_does_nothing():
     q, k, v, wq, wk = [_cuda(t) for t in _case(1, 1, 4, 2, 64)]
     cos, sin = [t.cuda() for t in _angles64(4, 64)]

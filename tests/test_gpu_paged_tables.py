@@ -107,6 +107,15 @@ def test_extend(B, bs, hi, new_hi, pad, in_place):
     _check_extend(lens, new, table, free, nf, bs, B * max_blocks + 5, sum(new) + pad, in_place)
 
 
+@pytest.mark.parametrize("B", [4010, 4011, 8192])
+def test_the_most_sequences(B):
+    """Around the batch that fills the shared memory a kernel has unasked, and the largest."""
+    lens, new, table, free, nf = _state(B, 16, 4, B * 4, B, 40, 5)
+    _check_extend(lens, new, table, free, nf, 16, B * 4, sum(new) + 3, in_place=True)
+    lens, _, table, free, nf = _state(B, 16, 4, B * 4, B + 1, 60, 0, extra=B * 4)
+    _check_release(lens, [b % 2 for b in range(B)], table, free, nf, 16, B * 4)
+
+
 def test_extend_fills_every_block_to_its_edge():
     # lengths around a block's end, new tokens around whole blocks
     lens = [0, 15, 16, 17, 31, 32, 0, 16, 47, 48]

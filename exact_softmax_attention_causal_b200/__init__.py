@@ -727,17 +727,20 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, pos
     w_bf16, rd, max_pos = _angles(q_weight, k_weight, cos, sin, positions, (B, N), d, dev)
     _need_status(status, dev)
     if dq is None and dk is None and dv is None:
-        fused = torch.empty((B, N, Hq + 2 * Hkv, d), dtype=bf16, device=dev)
-        dq, dk, dv = fused[:, :, :Hq], fused[:, :, Hq:Hq + Hkv], fused[:, :, Hq + Hkv:]
-    dq = torch.empty((B, N, Hq, d), dtype=bf16, device=dev) if dq is None else dq
-    dk = torch.empty((B, N, Hkv, d), dtype=bf16, device=dev) if dk is None else dk
-    dv = torch.empty((B, N, Hkv, d), dtype=bf16, device=dev) if dv is None else dv
-    _need_heads_out(dq, "dq", (B, N, Hq, d), dev)
-    _need_heads_out(dk, "dk", (B, N, Hkv, d), dev)
-    _need_heads_out(dv, "dv", (B, N, Hkv, d), dev)
+        heads = Hq + 2 * Hkv
+        dq, dk, dv = torch.empty((B, N, heads, d), dtype=bf16, device=dev).split_with_sizes((Hq, Hkv, Hkv), 2)
+        grad_strides = _strides(*(N * heads * d, heads * d, d) * 3)
+    else:
+        dq = torch.empty((B, N, Hq, d), dtype=bf16, device=dev) if dq is None else dq
+        dk = torch.empty((B, N, Hkv, d), dtype=bf16, device=dev) if dk is None else dk
+        dv = torch.empty((B, N, Hkv, d), dtype=bf16, device=dev) if dv is None else dv
+        _need_heads_out(dq, "dq", (B, N, Hq, d), dev)
+        _need_heads_out(dk, "dk", (B, N, Hkv, d), dev)
+        _need_heads_out(dv, "dv", (B, N, Hkv, d), dev)
+        grad_strides = _strides(*dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3])
     dwq = dwk = None
     if q_weight is not None:
-        dwq, dwk = torch.empty((2, d), dtype=torch.float32, device=dev).unbind()
+        dwq, dwk = torch.empty(2 * d, dtype=torch.float32, device=dev).unsafe_split_with_sizes((d, d))
         if workspace is None:
             workspace = torch.empty(qk_norm_rope_backward_workspace_bytes(B, N, Hq, Hkv, d), dtype=torch.uint8,
                                     device=dev)
@@ -745,7 +748,7 @@ def qk_norm_rope_backward(q, k, q_weight, k_weight, cos, sin, d_q, d_k, d_v, pos
     rc = _lib.lib().attn_qk_norm_rope_backward(
         q.data_ptr(), k.data_ptr(), _strides(*q.stride()[:3], *k.stride()[:3]), _addr(q_weight), _addr(k_weight),
         w_bf16, cos.data_ptr(), sin.data_ptr(), _addr(positions), d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(),
-        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _strides(*dq.stride()[:3], *dk.stride()[:3], *dv.stride()[:3]),
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), grad_strides,
         _addr(dwq), _addr(dwk), B, N, Hq, Hkv, d, rd, max_pos, float(eps), int(interleaved), _addr(workspace),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _addr(status), _current(dev))
     _lib.check(rc, "attn_qk_norm_rope_backward")

@@ -443,7 +443,7 @@ size_t attn_qk_norm_rope_backward_workspace_bytes(int B, int N, int Hq, int Hkv,
   if (B <= 0 || N <= 0 || Hq <= 0 || Hkv <= 0 || (d != 64 && d != 128)) return 0;
   int sms = 0;
   if (current_sm_count(&sms) != ATTN_OK) return 0;
-  return norm_rope_bwd_workspace(norm_rope_bwd_plan(static_cast<long long>(B) * N, Hq, Hkv, d, sms), d);
+  return norm_rope_bwd_workspace(norm_rope_bwd_ctas(static_cast<long long>(B) * N, Hq, Hkv, d, sms), d);
 }
 
 int attn_qk_norm_rope_backward(const void* q, const void* k, const int64_t* strides, const void* q_weight,
@@ -471,13 +471,13 @@ int attn_qk_norm_rope_backward(const void* q, const void* k, const int64_t* stri
     if (sb[t] % 8 != 0 || sn[t] % 8 != 0 || sh[t] % 8 != 0) return ATTN_ERR_INVALID_ARG;
   }
   if (current_sm_count(&a.sms) != ATTN_OK) return ATTN_ERR_CUDA;
-  const NormRopeBwdPlan plan = norm_rope_bwd_plan(static_cast<long long>(B) * N, Hq, Hkv, d, a.sms);
+  const int ctas = norm_rope_bwd_ctas(static_cast<long long>(B) * N, Hq, Hkv, d, a.sms);
   if (norm &&
-      (!workspace || !aligned16(workspace) || workspace_bytes < norm_rope_bwd_workspace(plan, d)))
+      (!workspace || !aligned16(workspace) || workspace_bytes < norm_rope_bwd_workspace(ctas, d)))
     return ATTN_ERR_WORKSPACE;
   const void* const dz[3] = {d_q, d_k, d_v};
   void* const dx[3] = {dq, dk, dv};
-  return launch_norm_rope_backward(a, dz, dx, sb, sn, sh, dq_weight, dk_weight, static_cast<float*>(workspace), plan,
+  return launch_norm_rope_backward(a, dz, dx, sb, sn, sh, dq_weight, dk_weight, static_cast<float*>(workspace), ctas,
                                    status, reinterpret_cast<cudaStream_t>(stream));
 }
 

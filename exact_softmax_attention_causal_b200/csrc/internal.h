@@ -142,17 +142,14 @@ struct NormRopeArgs {
   float eps;
 };
 int norm_rope_chunks(int Hq, int Hkv);  // groups of head rows per token
-// The backward pass: CTAs side by side over the tokens, and parts the heads are dealt in.
-struct NormRopeBwdPlan {
-  int strips, parts;
-};
-NormRopeBwdPlan norm_rope_bwd_plan(long long tokens, int Hq, int Hkv, int d, int sms);
-size_t norm_rope_bwd_workspace(const NormRopeBwdPlan& plan, int d);
+// CTAs of the backward pass, and the bytes of their parts of the weight gradients.
+int norm_rope_bwd_ctas(long long tokens, int Hq, int Hkv, int d, int sms);
+size_t norm_rope_bwd_workspace(int ctas, int d);
 // slots null: outputs [B, H, N, d]; else q [T, Hq, d], k and v into the pools.
 int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_out, const int32_t* slots,
                      long long num_slots, int32_t* status, cudaStream_t stream);
 int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], void* const dx[3], const int64_t dsb[3],
                               const int64_t dsn[3], const int64_t dsh[3], float* dwq, float* dwk, float* dw_part,
-                              const NormRopeBwdPlan& plan, int32_t* status, cudaStream_t stream);
+                              int ctas, int32_t* status, cudaStream_t stream);
 
 }  // namespace attn

@@ -29,8 +29,9 @@
 // heads, d = 128 (forward 405 MB, backward 573 MB): one group per 4 heads of a
 // token, groups on a token's heads 113 and 168 us; groups on consecutive tokens
 // 80 and 127; all heads of a token in turn 71 and 120; the steps prefetched 66
-// (93 % of HBM) and 108; the backward's two sums a row taken side by side 104 (84 %;
-// more warps an SM, at 80 registers, and a third step in the ring are both slower).
+// (93 % of HBM) and 108; the backward's two sums a row taken side by side 104, its
+// CTAs' shares even in rows moved 99 (88 %; more warps an SM, at 80 registers, and a
+// third step in the ring both take 104).
 //
 // All arithmetic is in 32 bits; the result is rounded to bf16 once. The weight
 // gradients are summed in 32 bits in a fixed order: over a thread's rows, the
@@ -322,23 +323,45 @@ struct NormRopeBwdParams {
   float* dw_part;  // a row of d for each CTA and weight: [2][gridDim.x][d]
   int32_t* status;
   unsigned tokens, tiles;
-  int N, Hq, Hkv, rd, max_pos, w_bf16, parts;
+  int N, Hq, Hkv, rd, max_pos, w_bf16;
   Chunks ch;
   float eps;
 };
 
-// CTA blockIdx.x: of the chunks a part, as in the forward pass, for every
-// (gridDim.x / parts)-th tile of tokens. Two CTAs an SM: three, at 80 registers,
-// took 111 us where two take 105.
+// The steps (a chunk of a tile of tokens, tile after tile) as a line of tensor
+// rows to move: dz, x and dx for a chunk of q or k, dz and dx for one of v or
+// without norms. Place `at` on it, rounded up to a step.
+struct Step {
+  unsigned tile;
+  int chunk;
+};
+template <bool NORM>
+__device__ __forceinline__ Step step_at(unsigned long long at, const Chunks& ch) {
+  constexpr int kTurned = NORM ? 3 : 2;
+  const int turned = ch.q + ch.kv, width = kTurned * turned + 2 * ch.kv;
+  Step s;
+  s.tile = static_cast<unsigned>(at / width);
+  const int in = static_cast<int>(at - static_cast<unsigned long long>(s.tile) * width);
+  s.chunk = in <= kTurned * turned ? (in + kTurned - 1) / kTurned : turned + (in - kTurned * turned + 1) / 2;
+  if (s.chunk == ch.all()) ++s.tile, s.chunk = 0;
+  return s;
+}
+
+// CTA blockIdx.x: its share of the line. Two CTAs an SM: three, at 80 registers,
+// took 105 us where two take 99. A share
+// ends where it ends: whole tiles for each part of the heads left some CTAs with
+// the norms and others with the copies (114 us where even shares take 104).
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int kLanes = D / 8;
   constexpr int kGroups = kNrThreads / kLanes;
   __shared__ float dw_s[kNrThreads / 32][D];
   const int lane = threadIdx.x & (kLanes - 1);
-  const unsigned first = blockIdx.x / p.parts, stride = gridDim.x / p.parts;
-  const int part = static_cast<int>(blockIdx.x - first * p.parts), all = p.ch.all();
-  const int c_begin = all * part / p.parts, c_end = all * (part + 1) / p.parts;
+  const int all = p.ch.all();
+  const unsigned long long line =
+      static_cast<unsigned long long>(p.tiles) * ((NORM ? 3 : 2) * (p.ch.q + p.ch.kv) + 2 * p.ch.kv);
+  const Step begin = step_at<NORM>(line * blockIdx.x / gridDim.x, p.ch);
+  const Step end = step_at<NORM>(line * (blockIdx.x + 1) / gridDim.x, p.ch);
   const int half_lanes = p.rd / 16;
   const bool turned = 8 * lane < p.rd;
   const int partner = (threadIdx.x & 31) + (!turned ? 0 : (lane >= half_lanes ? -half_lanes : half_lanes));
@@ -367,12 +390,11 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
   Ring<2 * kHeads> ring(ring_smem);  // dz's pieces, then x's
   int slot_at = 0, slot_in = 0;
   // the step to fetch next: a chunk of a tile
-  unsigned f_tile = first;
-  int f_chunk = c_begin;
-  Place fp = place(first < p.tiles ? first : 0);
+  Step f = begin;
+  Place fp = place(begin.tile);
   auto fetch = [&]() {
-    if (f_tile < p.tiles) {
-      const HeadRange hr = heads_of(p.ch, f_chunk, p.Hq, p.Hkv);
+    if (f.tile < end.tile || (f.tile == end.tile && f.chunk < end.chunk)) {
+      const HeadRange hr = heads_of(p.ch, f.chunk, p.Hq, p.Hkv);
       const __nv_bfloat16* zs =
           p.dz[hr.t] + ((fp.b * (hr.t == 0 ? p.Hq : p.Hkv) + hr.h0) * p.N + fp.n) * D + 8 * lane;
       const long long zstep = static_cast<long long>(p.N) * D;
@@ -387,17 +409,18 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
           if (i < hr.cnt) ring.load(slot_in, kHeads + i, xs + i * v.sh);
       }
       slot_in = next_slot(slot_in);
-      if (++f_chunk == c_end) {
-        f_chunk = c_begin;
-        f_tile += stride;
-        if (f_tile < p.tiles) fp = place(f_tile);
+      if (++f.chunk == all) {
+        f.chunk = 0;
+        fp = place(++f.tile);
       }
     }
     cp_async_commit();
   };
 #pragma unroll
   for (int i = 0; i < kSteps - 1; ++i) fetch();
-  for (unsigned tile = first; tile < p.tiles; tile += stride) {
+  for (unsigned tile = begin.tile; tile <= end.tile; ++tile) {
+    const int c_begin = tile == begin.tile ? begin.chunk : 0, c_end = tile == end.tile ? end.chunk : all;
+    if (c_begin >= c_end) break;  // the share ends with the tile before
     const Place pl = place(tile);
     const bool live = pl.live;
     const unsigned tok = pl.tok;
@@ -582,30 +605,14 @@ int launch_bwd_t(const NormRopeBwdParams& p, int ctas, float* dwq, float* dwk, c
 
 int norm_rope_chunks(int Hq, int Hkv) { return chunks_of(Hq, Hkv).all(); }
 
-// One wave of CTAs, `strips` of them side by side for each part of the heads:
-// the split that keeps most of the wave busy to the end (for 1,024 tiles on 148
-// SMs 296 strips of all heads would take 4 turns, the last one for 136 of them).
-NormRopeBwdPlan norm_rope_bwd_plan(long long tokens, int Hq, int Hkv, int d, int sms) {
+// One wave of CTAs, or one for each step of a small call.
+int norm_rope_bwd_ctas(long long tokens, int Hq, int Hkv, int d, int sms) {
   const long long groups = kNrThreads / (d / 8);
-  const long long tiles = (tokens + groups - 1) / groups;
+  const long long steps = (tokens + groups - 1) / groups * norm_rope_chunks(Hq, Hkv);
   const long long wave = static_cast<long long>(kBwdCtasPerSm) * sms;
-  const int all = norm_rope_chunks(Hq, Hkv);
-  NormRopeBwdPlan best{1, 1};
-  double busy = 0.;
-  for (int parts = 1; parts <= all && parts <= wave; ++parts) {
-    const long long strips = tiles < wave / parts ? tiles : wave / parts;
-    const long long turns = (tiles + strips - 1) / strips;
-    const double share = static_cast<double>(tiles) * parts / (static_cast<double>(turns) * wave);
-    if (share > busy * 1.02) {  // more parts read the angles more often
-      busy = share;
-      best = NormRopeBwdPlan{static_cast<int>(strips), parts};
-    }
-  }
-  return best;
+  return static_cast<int>(steps < wave ? steps : wave);
 }
-size_t norm_rope_bwd_workspace(const NormRopeBwdPlan& plan, int d) {
-  return static_cast<size_t>(plan.strips) * plan.parts * 2 * d * sizeof(float);
-}
+size_t norm_rope_bwd_workspace(int ctas, int d) { return static_cast<size_t>(ctas) * 2 * d * sizeof(float); }
 
 int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_out, const int32_t* slots,
                      long long num_slots, int32_t* status, cudaStream_t stream) {
@@ -638,10 +645,8 @@ int launch_norm_rope(const NormRopeArgs& a, void* q_out, void* k_out, void* v_ou
 
 int launch_norm_rope_backward(const NormRopeArgs& a, const void* const dz[3], void* const dx[3], const int64_t dsb[3],
                               const int64_t dsn[3], const int64_t dsh[3], float* dwq, float* dwk, float* dw_part,
-                              const NormRopeBwdPlan& plan, int32_t* status, cudaStream_t stream) {
+                              int ctas, int32_t* status, cudaStream_t stream) {
   NormRopeBwdParams p{};
-  const int ctas = plan.strips * plan.parts;
-  p.parts = plan.parts;
   for (int t = 0; t < 2; ++t)
     p.x[t] = HeadView{static_cast<const __nv_bfloat16*>(a.x[t]), a.sb[t], a.sn[t], a.sh[t]};
   for (int t = 0; t < 3; ++t) {

@@ -428,8 +428,8 @@ ATTN_API size_t attn_prefill_paged_varlen_workspace_bytes(int d);
  * Device checks (ATTN_STATUS_BIT_DEVICE_CHECK): a sequence with rows and a
  * length below their number or above max_seq_len, or with offsets out of order
  * or past T, gets NaN rows (those inside the tensor); a table entry outside the
- * pool gives NaN in the rows that need it, a sink logit of NaN or +infinity in
- * its head's.
+ * pool gives NaN in the rows that see a key of its block and in no other, a sink
+ * logit of NaN or +infinity in its head's.
  *
  * Errors (nothing is launched): ATTN_ERR_INVALID_ARG for NULL or misaligned
  * pointers, bad sizes, Hq % Hkv != 0, a table row shorter than max_seq_len, a

@@ -997,8 +997,14 @@ __global__ void __launch_bounds__(kVlThreads, 1)
         VlWalk w = first_walk();
         for (int it = 0;; ++it) {
           const int e = it % kPieces;
-          if (it >= kPieces && !mbar_wait_bounded(bar(kVbPieceDone + e), (it / kPieces - 1) & 1, budget, abort_flag))
+          // The piece that holds the entry (pieces_s[e] until it is given back) may take as
+          // long as its tiles do, each a chain of at most 8 waits: so many budgets, where
+          // every other wait is for one step of the pipeline.
+          if (it >= kPieces && !mbar_wait_bounded(bar(kVbPieceDone + e), (it / kPieces - 1) & 1,
+                                                  min(budget, 1LL << 35) * 8 * (pieces_s[e].nt + 2), abort_flag)) {
+            raise_abort(abort_flag, p.status);
             break;
+          }
           VlPiece pc;
           next_piece<D>(p, pl, cta, w, pc);
           pieces_s[e] = pc;

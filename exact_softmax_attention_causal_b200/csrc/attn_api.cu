@@ -149,8 +149,10 @@ int attn_prefill_paged_varlen(const void* q, const void* k_cache, const void* v_
   if (block_size != 16 && block_size != 32 && block_size != 64 && block_size != 128) return ATTN_ERR_UNSUPPORTED;
   // row indices are int32; positions leave room for a window's and a tile's width
   if (static_cast<long long>(T) * Hq > (1LL << 31) - 1 || max_seq_len > (1 << 30)) return ATTN_ERR_UNSUPPORTED;
-  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && window >= max_seq_len) mask_kind = ATTN_MASK_CAUSAL, n_sink = 0;
-  if (n_sink > max_seq_len) n_sink = max_seq_len;
+  // Window and sinks that leave no gap hide nothing: a key behind the sinks is at most max_seq_len - 1 - n_sink back.
+  // The others add up to less than 2^30, so the kernel's counts of keys fit 32 bits.
+  if (mask_kind == ATTN_MASK_SLIDING_WINDOW && static_cast<long long>(window) + n_sink >= max_seq_len)
+    mask_kind = ATTN_MASK_CAUSAL, n_sink = 0;
   int sms = 0;
   if (current_sm_count(&sms) != ATTN_OK) return ATTN_ERR_CUDA;
   if (!workspace || !aligned16(workspace) || workspace_bytes < varlen_workspace_bytes(d, sms))

@@ -53,3 +53,35 @@ def test_a_piece_may_take_longer_than_a_wait(monkeypatch):
         sl = 2.0 ** -18 * (big + 1 + rl.abs()) + c * 2.0 ** -24
         assert ((o[:, rows].double() - ro).abs() <= so + c * 2.0 ** -24 * spread).all()
         assert ((lse[:, rows].double() - rl).abs() <= sl).all()
+
+
+@pytest.mark.parametrize("window,n_sink,hidden", [(2 ** 30 - 1, 2 ** 30, 0), (2 ** 30 - 1, 2 ** 31 - 1, 0), (1, 2 ** 30 - 1, 0),
+                                                  (2 ** 29, 2 ** 29, 0), (2 ** 29, 2 ** 29 - 128, 128)])
+def test_window_and_sinks_of_the_longest_sequence(window, n_sink, hidden):
+    """The newest of 2^30 positions, every block the same, scores of 0: the output is the mean of V, the logarithm of
+    the sum that of the number of visible keys. Counts are whole numbers, exact in fp32 up to 2^24 of a multiprocessor's
+    stretch; the join adds under 200 of them, 2^-24 of the sum each."""
+    bs, d, c = 128, 64, 2 ** 30
+    kc = torch.zeros((2, bs, 1, d), dtype=BF16, device="cuda")
+    vc = torch.zeros_like(kc)
+    t, e = torch.arange(bs, device="cuda")[:, None], torch.arange(d, device="cuda")[None]
+    vc[1, :, 0] = ((t * (e + 1)) % 7 < 3).to(BF16)
+    table = torch.ones((2, c // bs), dtype=I32, device="cuda")
+    if hidden:  # the one block that the newest position does not see
+        table[0, (c - window - hidden) // bs] = -1
+    cu, lens = torch.tensor([0, 1, 6], dtype=I32, device="cuda"), torch.tensor([c, 40], dtype=I32, device="cuda")
+    q = torch.ones((6, 2, d), dtype=BF16, device="cuda")
+    status = torch.zeros(1, dtype=I32, device="cuda")
+    o, lse = prefill_paged_varlen(q, kc, vc, table, cu, lens, c, mask="window", window=window, n_sink=n_sink, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    mean = vc[1, :, 0].double().mean(0)
+    slack = 200 * 2.0 ** -24
+    assert ((o[0].double() - mean).abs() <= (2.0 ** -8 + slack) * mean).all()
+    assert ((lse[0].double() - math.log(c - hidden)).abs() <= slack + 2.0 ** -18 * 22).all()
+    for i in range(5):  # the short sequence beside it: positions 35 to 39
+        seen = torch.arange(36 + i, device="cuda")
+        seen = seen[(35 + i - seen < window) | (seen < n_sink)]
+        mean = vc[1, seen, 0].double().mean(0)
+        assert ((o[1 + i].double() - mean).abs() <= (2.0 ** -8 + slack) * mean).all()
+        assert ((lse[1 + i].double() - math.log(len(seen))).abs() <= slack + 2.0 ** -18 * 5).all()

@@ -34,8 +34,12 @@
 // third step in the ring both take 104).
 //
 // All arithmetic is in 32 bits; the result is rounded to bf16 once. The weight
-// gradients are summed in 32 bits in a fixed order: over a thread's rows, the
-// CTA's lanes, then the CTAs' partial sums by a second kernel. No atomics.
+// gradients are summed in 32 bits in a fixed order: the 4 rows of a step, a
+// thread's steps one after another, the CTA's lanes, then the CTAs' partial sums by
+// a second kernel. No atomics. So their rounding is at most 2^-24 of the sum of
+// |dy n| for each of a thread's steps (42 for the training shapes above, in
+// proportion to tokens and heads beyond one wave of CTAs) and for each of some 60
+// additions after them.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -219,6 +219,16 @@ int decode_common(const void* q, const void* k_cache, const void* v_cache, const
     return ATTN_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < decode_workspace_bytes(B, Hq, Hkv, d, plan))
     return ATTN_ERR_WORKSPACE;
+  // A captured call keeps its tag on every replay, so the counters would hold the last replay's counts: its graph
+  // clears them first.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(reinterpret_cast<cudaStream_t>(stream), &capture) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (capture != cudaStreamCaptureStatusNone && plan.splits > 1) {
+    const DecodeWorkspace ws = decode_workspace_layout(B, Hq, Hkv, d, plan);
+    if (cudaMemsetAsync(static_cast<uint8_t*>(workspace) + ws.counters_offset, 0, ws.bytes - ws.counters_offset,
+                        reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return ATTN_ERR_CUDA;
+  }
   const cudaError_t e = launch_decode(q, k_cache, v_cache, block_table, seq_lens, sinks, o, lse, B, Hq, Hkv, d,
                                       num_blocks, block_size, max_blocks_per_seq, max_seq_len, window, n_sink, scale,
                                       workspace, plan, status, reinterpret_cast<cudaStream_t>(stream));

@@ -219,7 +219,8 @@ ATTN_API size_t attn_decode_workspace_bytes(int B, int Hq, int Hkv, int d, int m
  *   workspace    device scratch of at least attn_decode_workspace_bytes(...)
  *                bytes, 16-byte aligned; contents on entry are irrelevant
  *                (the counters carry a 32-bit tag that changes with every
- *                call; a counter without this call's tag is taken as zero).
+ *                call; a counter without this call's tag is taken as zero; a call
+ *                captured into a CUDA graph clears them in the graph).
  *                Calls whose kernels overlap on the GPU must not share a
  *                workspace.
  *   status       device int32 or NULL.

@@ -463,7 +463,10 @@ def prefill_paged_varlen(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_s
     [cu_q[b], cu_q[b + 1]), its newest positions; seq_lens [B] int32 counts its
     cached tokens, the new ones included. window, n_sink and sinks as in
     decode_paged_window(), with mask="window". Rows outside [cu_q[0], cu_q[B])
-    of a given out and lse stay as they were (else they are undefined).
+    of a given out and lse stay as they were (else they are undefined). For single
+    tokens alone with up to 8 query heads per K/V head decode_paged() and
+    decode_paged_window() are quicker, for equal chunks of 512 rows and more
+    prefill_paged().
     """
     if not _here(q, stream):
         return _elsewhere(prefill_paged_varlen, q, locals())

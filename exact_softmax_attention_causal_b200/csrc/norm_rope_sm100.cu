@@ -26,12 +26,13 @@
 // of consecutive tokens: a head's rows then lie together on the [B, H, N, d] side
 // (4 KB at d = 128), a token's heads on the other (1 KB), and angles and weights
 // are read once for all heads of the CTA. Measured for B = 4, N = 4096, 32 / 8
-// heads, d = 128 (forward 405 MB, backward 573 MB): one group per 4 heads of a
-// token, groups on a token's heads 113 and 168 us; groups on consecutive tokens
-// 80 and 127; all heads of a token in turn 71 and 120; the steps prefetched 66
-// (93 % of HBM) and 108; the backward's two sums a row taken side by side 104, its
-// CTAs' shares even in rows moved 99 (88 %; more warps an SM, at 80 registers, and a
-// third step in the ring both take 104).
+// heads, d = 128 (forward 405 MB, backward 573 MB), all forms in turn on one card,
+// three sets of inputs in turn, medians: one group per 4 heads of a token, groups on
+// a token's heads 117 and 168 us; groups on consecutive tokens 85 and 131; all heads
+// of a token in turn 76 and 127; the steps prefetched 69 (89 % of HBM) and 116; the
+// backward's two sums a row taken side by side 112, its CTAs' shares even in rows
+// moved 100 (87 %; a third CTA an SM, at 80 registers, takes 112, a third step in the
+// ring 106).
 //
 // All arithmetic is in 32 bits; the result is rounded to bf16 once. The weight
 // gradients are summed in 32 bits in a fixed order: the 4 rows of a step, a
@@ -351,10 +352,9 @@ __device__ __forceinline__ Step step_at(unsigned long long at, const Chunks& ch)
   return s;
 }
 
-// CTA blockIdx.x: its share of the line. Two CTAs an SM: three, at 80 registers,
-// took 105 us where two take 99. A share
-// ends where it ends: whole tiles for each part of the heads left some CTAs with
-// the norms and others with the copies (114 us where even shares take 104).
+// CTA blockIdx.x: its share of the line. Two CTAs an SM (figures at the file's
+// head). A share ends where it ends: whole tiles for each part of the heads left some
+// CTAs with the norms and others with the copies.
 template <int D, bool INTER, bool NORM>
 __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kernel(const NormRopeBwdParams p) {
   constexpr int kLanes = D / 8;
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kNrThreads, kBwdCtasPerSm) norm_rope_bwd_kerne
           unpack8(ring.get(slot_at, kHeads + i), x);
 #pragma unroll
           for (int e = 0; e < 4; ++e) gw[e] = fmul2(g[e], w[e]);
-          // sum(g x) r in place of sum(g n): the two sums do not wait for each other (107.7 -> 103.6 us)
+          // sum(g x) r in place of sum(g n): the two sums do not wait for each other
           const float ss = group_sum<kLanes>(dot8(x, x)), gx = group_sum<kLanes>(dot8(gw, x));
           const float r = rsqrtf(ss * (1.f / D) + p.eps);
           const float t = -(gx * r) * (1.f / D) * r;  // n mean(g n) = -t x

@@ -25,18 +25,22 @@
 // partial outputs (fp32, unnormalised, with each row's maximum and sum), which
 // a second, small grid joins in a fixed order: nothing depends on timing. A CTA
 // has at most two partials, one per end, so the workspace does not depend on
-// the batch.
+// the batch. The line counts n_sink's tiles and one more for every item under a
+// window, also where the window still reaches position 0: with sinks longer than some
+// of the sequences the dealing gets uneven (a batch half of short sequences, window
+// 128: the busiest CTA 14 % above the mean at n_sink = 200, 34 % at 1,000, else 4-9 %).
 //
 // What bounds it. Narrow items: HBM (64 KB of K and V a tile at d = 128, 1.45 us of
 // an SM's share of HBM, against 0.55 us of MMAs); at d = 64 the chain scores ->
 // softmax -> P V -> scores of the two teams. Wide items: that chain, the softmax's
 // exponentials and the tensor cores in turn, as in the prefill kernel. Short items
 // (a window of 128): the latency of an item's steps, 13,000 cycles for two tiles.
-// Measured: 64 sequences of 1K-32K tokens with 1-8 rows each, 32 / 8 heads, d = 128
-// 640 us (6,610 GB/s, the copy's rate); one of 131,072 tokens 105 us (5,100 GB/s);
-// 4 chunks of 2,048 rows on 16,384 tokens 1,860 us (1,110 TFLOP/s); 4 chunks of
-// 1K-2K rows beside 32 single rows 1,140 us; 48 chunks of up to 512 rows and 16
-// single ones, window 128, 64 / 8 heads, d = 64 214 us.
+// Measured, in passes one after another for a second, at the power cap, and in runs of
+// a few passes: 64 sequences of 1K-32K tokens with 1-8 rows each, 32 / 8 heads, d = 128
+// 703 and 645 us (6,020 and 6,560 GB/s); one of 131,072 tokens 109 and 104 us (4,920
+// and 5,180 GB/s); 4 chunks of 2,048 rows on 16,384 tokens 2,177 and 1,867 us (947 and
+// 1,104 TFLOP/s); 4 chunks of 1K-2K rows beside 32 single rows 1,360 and 1,155 us; 48
+// chunks of up to 512 rows and 16 single ones, window 128, 64 / 8 heads, d = 64 216 us.
 //
 // Roles, pipeline and the lazily moved maximum are those of the prefill kernel
 // (prefill_sm100.cu): 8 softmax warps, an MMA warp, here two TMA warps (K and V),
@@ -44,7 +48,7 @@
 // team was slower: their products wait for one another in the tensor cores' queue,
 // 4,400 cycles a wide tile instead of 3,450.) Probabilities go to the second
 // product as bf16 (the tensor cores take nothing wider at this
-// rate; 2^-9 of each p, averaged over the row), sums and outputs stay in fp32.
+// rate; at most 2^-8 of each p, averaged over the row), sums and outputs stay in fp32.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -403,7 +403,11 @@ ATTN_API size_t attn_prefill_paged_varlen_workspace_bytes(int d);
  * table ("Module 09", "Chunked Prefill" and continuous batching: chunks of
  * prompts and decoding sequences in one batch). Query row i of sequence b sits
  * at position seq_lens[b] - n_b + i; masks as in attn_prefill_paged, with the
- * sink positions and learned sink logits of attn_decode_paged_window.
+ * sink positions and learned sink logits of attn_decode_paged_window. Scores,
+ * sums and partial outputs are fp32; probabilities enter the product with V as
+ * bf16 (off by 2^-8 of each at most, as in attn_prefill), O is rounded to bf16 once.
+ * Rows of single tokens alone are quicker in the decodes with up to 8 query heads
+ * per K/V head, equal chunks of 512 rows and more in attn_prefill_paged.
  *
  *   q            [T, Hq, d] bf16, rows of all sequences packed   read
  *   k_cache,

@@ -425,26 +425,31 @@ struct VRing {
   }
 };
 
-// Whether the row at position `pos` (below nk) sees a key of the piece in a block whose table
-// entry is outside the pool. Only pieces with such an entry ask (a row for each lane:
-// the entries are the same for all of a warp), so the key loop pays nothing for it.
-__device__ __forceinline__ bool sees_bad_entry(const VarlenParams& p, const VlPiece& pc, int pos) {
+// Whether this lane's row, at position `pos`, sees a key of the piece in a block whose
+// table entry is outside the pool (warp-collective: a lane looks at every 32nd block,
+// then all rows at each bad one). Only pieces with such an entry ask, so the key loop
+// pays nothing for it.
+__device__ __forceinline__ bool sees_bad_entry(const VarlenParams& p, const VlPiece& pc, int pos, int lane) {
   const bool win = p.mask_kind == ATTN_MASK_SLIDING_WINDOW;
   const int hi = p.mask_kind == ATTN_MASK_FULL ? pc.nk - 1 : pos, lo = win ? pos - p.window + 1 : 0;
   const int sink = win ? p.n_sink : 0;
+  const int bs = p.block_size, per = kBN / bs, blocks = pc.nt * per;
   const int32_t* row = p.block_table + static_cast<size_t>(pc.b) * p.max_blocks;
-  bool bad = false;
+  bool sees = false;
 #pragma unroll 1
-  for (int j = pc.j0; j < pc.j0 + pc.nt; ++j) {
-    const int k0 = pc.g.tile_key(j);
-#pragma unroll 1
-    for (int key = k0; key < k0 + kBN && key <= hi; key += p.block_size) {
-      if (key + p.block_size <= lo && key >= sink) continue;
-      const int ent = __ldg(row + key / p.block_size);
-      bad |= ent < 0 || ent >= p.num_blocks;
+  for (int i0 = 0; i0 < blocks; i0 += 32) {
+    const int i = i0 + lane, key = pc.g.tile_key(pc.j0 + i / per) + i % per * bs;
+    bool bad = false;
+    if (i < blocks && key < pc.g.key_end && (key + bs > pc.g.key_lo || key < pc.g.sink_end)) {  // as the copies ask
+      const int ent = __ldg(row + key / bs);
+      bad = ent < 0 || ent >= p.num_blocks;
+    }
+    for (unsigned who = __ballot_sync(0xffffffffu, bad); who != 0; who &= who - 1) {
+      const int k = __shfl_sync(0xffffffffu, key, __ffs(who) - 1);
+      sees |= k <= hi && (k + bs > lo || k < sink);
     }
   }
-  return bad;
+  return sees;
 }
 
 // Every (row, key) pair of a tile is visible: rows at positions [qa, qb], keys [k0, k0 + 128).
@@ -1155,9 +1160,9 @@ __global__ void __launch_bounds__(kVlThreads, 1)
       }
 
       const bool whole = pc.whole;
-      const bool bad = bad_s[it % kPieces] != 0;
+      const bool bad = __any_sync(0xffffffffu, bad_s[it % kPieces] != 0);
       if (bad && lane == 0 && p.status != nullptr) atomicOr(p.status, ATTN_STATUS_BIT_DEVICE_CHECK);
-      float l = !ok || (bad && row_valid && sees_bad_entry(p, pc, qa + rtok)) ? NAN : l_sum, norm = 1.f;
+      float l = !ok || (bad && sees_bad_entry(p, pc, qa + rtok, lane)) ? NAN : l_sum, norm = 1.f;
       if (whole) {
         float m = m_used, ff = 1.f;
         if (p.sinks != nullptr) {  // one more column with no value
